@@ -115,6 +115,8 @@ extern "C" {
 #define DSEL_ERR_DEVICE_TIMEOUT (-14) /* a kernel gave up a bounded wait (see dsel_device_status) */
 #define DSEL_ERR_UNAVAILABLE (-15) /* the entry point is not part of this build */
 #define DSEL_ERR_SCRATCH_LIMIT (-16) /* dsel_topk_noalloc: the call needs more than its static scratch */
+#define DSEL_ERR_SHAPE (-17)       /* a size or count outside what the operator takes */
+#define DSEL_ERR_OVERLAP (-18)     /* the output shares memory with the input in a way that is not allowed */
 
 /* Size of the static device scratch behind dsel_topk_noalloc (512 KiB per device). */
 #define DSEL_NOALLOC_SCRATCH_BYTES (512 * 1024)
@@ -298,6 +300,55 @@ DSEL_API int dsel_shard_stack(const void* vals_in, const int64_t* idx_in, int dt
  */
 DSEL_API int dsel_take_index(const int64_t* table, int64_t table_stride, const void* pos, int pos_dtype, int64_t rows,
                              int32_t k, int index_dtype, void* indices_out, void* stream);
+
+/*
+ * dsel_logits -- penalties for repeated tokens, biases and a grammar mask on the
+ * logits of a batch, written as float32 rows that dsel_topk (DSEL_F32) and
+ * dsel_topk_sample take as they are, without `end`.
+ *
+ * For row r and token v, with seen(v): v occurs among the row's tokens, and
+ * c(v): how often it occurs among those of its answer:
+ *   1. y = float(x[r][v]); seen(v): y = y > 0 ? y / repetition[r] : y * repetition[r]
+ *   2. y = y - frequency[r] * c(v) - presence[r] * (c(v) > 0 ? 1 : 0)
+ *   3. y = y + the row's biases of v (an entry that occurs twice counts twice)
+ *   4. y = -inf where the row's mask has a 0 at v, whatever y was (NaN too)
+ *   out[r][v] = y; out[r][vocab .. out_stride) = -inf
+ * in float32, biases in list order: the result does not depend on scheduling.
+ * A row whose mask leaves nothing holds only -inf (dsel_topk_sample then draws
+ * uniformly among its first k).
+ *
+ *   x            device, rows x x_stride elements of `dtype` (DSEL_BF16 / DSEL_F32),
+ *                x_stride >= vocab; aligned to its element
+ *   tokens       device [rows][tokens_stride], int32 or int64 (token_dtype: DSEL_I32 /
+ *                DSEL_I64), or NULL (no penalties).  Row r's tokens so far are its
+ *                first total_len[r] (clamped to [0, width]; NULL: width), the first
+ *                prompt_len[r] of them the prompt, the others its answer (NULL: all of
+ *                them).  Ids outside [0, vocab) are ignored.
+ *   repetition, frequency, presence
+ *                device float32 [rows], each may be NULL: 1, 0, 0.  The tokens of a
+ *                row with neutral values are not read.
+ *   bias_offsets, bias_ids, bias_values, bias_count
+ *                row r's biases are the entries bias_offsets[r] .. bias_offsets[r + 1]
+ *                (int32 [rows + 1], clamped to [0, bias_count]) of int32 ids and float32
+ *                values; all NULL: none.  Ids outside [0, vocab) are ignored.
+ *   mask, mask_stride, mask_count, mask_rows
+ *                device, mask_count rows of mask_stride 32-bit words; bit v % 32 of
+ *                word v / 32 set: token v is allowed.  Row r uses mask row
+ *                mask_rows[r] (int32 [rows]; outside [0, mask_count): the row is not
+ *                masked), or row r where mask_rows is NULL.  mask NULL: none.
+ *   out          device float32 [rows][out_stride], 16-byte aligned; out_stride >= vocab, a
+ *                multiple of dsel_stride_requirement(DSEL_F32).  May be x itself
+ *                (DSEL_F32, the same stride); other overlaps return DSEL_ERR_OVERLAP.
+ * Returns DSEL_OK, DSEL_ERR_DTYPE / _ROWS / _SHAPE / _STRIDE / _INDEX_DTYPE / _NULL /
+ * _ALIGN / _OVERLAP / _DEVICE or DSEL_ERR_CUDA.  One launch, asynchronous on
+ * `stream`, no workspace; can be captured.
+ */
+DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, int64_t x_stride, const void* tokens,
+                         int token_dtype, int32_t width, int64_t tokens_stride, const int32_t* prompt_len,
+                         const int32_t* total_len, const float* repetition, const float* frequency,
+                         const float* presence, const int32_t* bias_offsets, const int32_t* bias_ids,
+                         const float* bias_values, int64_t bias_count, const void* mask, int64_t mask_stride,
+                         int64_t mask_count, const int32_t* mask_rows, float* out, int64_t out_stride, void* stream);
 
 /* Row-stride requirement in elements for `dtype` (the pages' get_stride_requirement,
  * narracomm paragraph on install and switches): 16 for both dtypes, so every row

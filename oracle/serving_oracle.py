@@ -1,0 +1,61 @@
+"""CPU oracles, in float64, of the operators before and after the TopK.
+TEST INFRASTRUCTURE, NOT PRODUCT: only ``tests/`` may import this module.
+
+Plain loops over rows, written from the formulas in ``include/dsel.h``; inputs are
+numpy arrays that already hold the values of the device tensors (float64 holds every
+float32, bfloat16, float16 and e4m3 value exactly).
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+def oracle_logits(x, stride, *, tokens=None, prompt_len=None, total_len=None, repetition=None, frequency=None,
+                  presence=None, biases=None, mask=None, mask_rows=None):
+    """Rows of ``process_logits`` and, beside them, the sum of the magnitudes that each value was
+    computed from and the number of roundings in float32 (for a bound on the device's error).
+
+    ``biases``: a list of (id, value) pairs per row.  Returns (y, magnitude, roundings), each
+    [rows, stride] float64."""
+    rows, vocab = x.shape
+    y = np.full((rows, stride), -np.inf)
+    mag = np.zeros((rows, stride))
+    rnd = np.zeros((rows, stride))
+    with np.errstate(invalid="ignore", over="ignore"):
+        for r in range(rows):
+            z = x[r].astype(np.float64).copy()
+            m, n = np.abs(z), np.zeros(vocab)
+            if tokens is not None:
+                total = tokens.shape[1] if total_len is None else min(max(int(total_len[r]), 0), tokens.shape[1])
+                prompt = 0 if prompt_len is None else int(prompt_len[r])
+                rep = 1.0 if repetition is None else float(repetition[r])
+                freq = 0.0 if frequency is None else float(frequency[r])
+                pres = 0.0 if presence is None else float(presence[r])
+                seen, count = set(), {}
+                for i in range(total):
+                    v = int(tokens[r, i])
+                    if 0 <= v < vocab:
+                        seen.add(v)
+                        if i >= prompt:
+                            count[v] = count.get(v, 0) + 1
+                for v in seen:
+                    z[v] = z[v] / rep if z[v] > 0 else z[v] * rep
+                    m[v] = max(m[v], abs(z[v]))
+                    n[v] += 1
+                for v, c in count.items():
+                    z[v] -= freq * c + pres
+                    m[v] += abs(freq * c) + abs(pres)
+                    n[v] += 3
+            for v, b in (biases[r] if biases is not None else []):
+                if 0 <= v < vocab:
+                    z[v] += float(b)
+                    m[v] += abs(float(b))
+                    n[v] += 2
+            if mask is not None:
+                at = r if mask_rows is None else int(mask_rows[r])
+                if 0 <= at < mask.shape[0]:
+                    for v in range(vocab):
+                        if not (int(mask[at, v // 32]) >> (v % 32)) & 1:
+                            z[v], m[v], n[v] = -np.inf, 0.0, 0.0
+            y[r, :vocab], mag[r, :vocab], rnd[r, :vocab] = z, m, n
+    return y, mag, rnd

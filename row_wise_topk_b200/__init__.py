@@ -28,6 +28,7 @@ DSEL_IDX_PAD, DSEL_IDX_NAN, DSEL_IDX_BAD_END = -1, -2, -3
 DSEL_KERNEL_STREAM, DSEL_KERNEL_RESIDENT, DSEL_KERNEL_SLICE = 0, 1, 2
 DSEL_OK = 0
 DSEL_ERR_SCRATCH_LIMIT = -16
+DSEL_ERR_SHAPE, DSEL_ERR_OVERLAP = -17, -18
 DSEL_NOALLOC_SCRATCH_BYTES = 512 * 1024
 
 
@@ -76,6 +77,10 @@ def _load() -> ctypes.CDLL:
     lib.dsel_shard_stack.argtypes = [vp, vp, c_int, c_i64, ctypes.c_int32, ctypes.c_int32, c_i64, c_i64, vp, vp, vp]
     lib.dsel_take_index.restype = c_int
     lib.dsel_take_index.argtypes = [vp, c_i64, vp, c_int, c_i64, ctypes.c_int32, c_int, vp, vp]
+    i32 = ctypes.c_int32
+    lib.dsel_logits.restype = c_int
+    lib.dsel_logits.argtypes = [vp, c_int, c_i64, i32, c_i64, vp, c_int, i32, c_i64, vp, vp, vp, vp, vp, vp, vp, vp,
+                                c_i64, vp, c_i64, c_i64, vp, vp, c_i64, vp]
     lib.dsel_stride_requirement.restype = c_i64
     lib.dsel_stride_requirement.argtypes = [c_int]
     lib.dsel_status_string.restype = ctypes.c_char_p
@@ -297,3 +302,7 @@ def topk_sample(logits, k: int, u, *, temperature: float = 1.0, top_p: float = 1
     if return_topk:
         return token, prob, (values, indices)
     return token, prob
+
+
+# the operators before and after the selection (same manner: torch tensors in, one library call)
+from .serving import process_logits  # noqa: E402,F401

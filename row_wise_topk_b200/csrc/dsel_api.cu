@@ -355,6 +355,8 @@ DSEL_API const char* dsel_status_string(int status) {
     case DSEL_ERR_SCRATCH_LIMIT:
       return "the split-row scratch this call needs exceeds the static scratch of dsel_topk_noalloc "
              "(DSEL_NOALLOC_SCRATCH_BYTES per device)";
+    case DSEL_ERR_SHAPE: return "a size or count is outside what the operator takes";
+    case DSEL_ERR_OVERLAP: return "the output overlaps the input in a way that is not allowed";
     default: return "unknown status";
   }
 }

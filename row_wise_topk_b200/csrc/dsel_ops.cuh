@@ -1,0 +1,72 @@
+// Shared by the operators around the TopK (logits processing, indexer scores,
+// sparse attention): launch helpers and thin PTX wrappers.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "dsel_plan.h"   // the C ABI (include/dsel.h) and the shape limits
+
+namespace dsel {
+
+// ---- host ----
+
+// The current device is an sm_100 GPU (asked once per device).
+inline int check_device() {
+  static int known[64];   // 0 unknown, 1 sm_100; written with the same value by every thread
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSEL_ERR_CUDA;
+  if (dev < 0 || dev >= 64) return DSEL_ERR_DEVICE;
+  if (known[dev] == 1) return DSEL_OK;
+  int major = 0, minor = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+    return DSEL_ERR_CUDA;
+  if (major != 10 || minor != 0) return DSEL_ERR_DEVICE;
+  known[dev] = 1;
+  return DSEL_OK;
+}
+
+// Lets `kern` use `bytes` of dynamic shared memory on the current device.
+inline cudaError_t allow_smem(const void* kern, int bytes) {
+  return bytes <= 48 * 1024 ? cudaSuccess
+                            : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// A launch in clusters of `cluster` CTAs that may begin while the launch before it
+// still runs: the kernel calls grid_wait() before it touches global memory.
+template <typename Kern, typename Params>
+cudaError_t launch_dependent(Kern kern, unsigned grid, int threads, int cluster, uint32_t smem, cudaStream_t st,
+                             const Params& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(unsigned(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// Whether [a, a + na * ea) and [b, b + nb * eb) share a byte.
+inline bool ranges_meet(const void* a, int64_t na, int ea, const void* b, int64_t nb, int eb) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  return pa < pb + uintptr_t(nb) * uintptr_t(eb) && pb < pa + uintptr_t(na) * uintptr_t(ea);
+}
+
+// ---- device ----
+
+// The launches before this one in the stream are complete and visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next launch may start its set-up.
+__device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+}  // namespace dsel

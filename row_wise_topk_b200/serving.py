@@ -1,0 +1,156 @@
+"""The operators before and after the TopK of a serving step, over torch tensors.
+
+``process_logits`` makes the rows that ``topk_sample`` (or ``topk``) takes: penalties
+for repeated tokens, biases, a grammar mask.
+
+Each is one call of the C ABI (``include/dsel.h`` states the formulas and the argument
+rules); this module checks the tensors and allocates the outputs.  Calls run on the
+tensors' device, on the current stream or on the raw handle given as ``stream``
+(outputs are then allocated for that stream).  Argument errors raise before any
+launch: ``TypeError`` / ``ValueError`` here, ``DselError`` from the library.
+"""
+from __future__ import annotations
+
+from . import DSEL_BF16, DSEL_F32, DSEL_I32, DSEL_I64, DSEL_OK, DselError, lib
+
+def _run(device, stream, call):
+    """``call(stream handle)`` with `device` current and, for a given stream, as torch's current one."""
+    import torch
+
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+            return call(stream)
+
+
+def _check(status):
+    if status != DSEL_OK:
+        raise DselError(status)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _vector(name, t, device, dtype, count):
+    """A contiguous 1-D tensor of `count` entries, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or t.dim() != 1 or (count is not None and t.shape[0] != count):
+        raise ValueError(f"{name} must be a 1-D {dtype} tensor on {device}"
+                         + ("" if count is None else f" with {count} entries"))
+    if not t.is_contiguous():   # a copy made here would run on another stream than the call
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _index_dtype(name, t):
+    import torch
+
+    if t.dtype == torch.int32:
+        return DSEL_I32
+    if t.dtype == torch.int64:
+        return DSEL_I64
+    raise TypeError(f"{name} must be int32 or int64")
+
+
+def _rows_of(name, t, device, rows):
+    """Row stride of a 2-D tensor whose rows are contiguous and do not overlap."""
+    if t.dim() != 2 or t.device != device or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be a 2-D tensor on {device}" + ("" if rows is None else f" with {rows} rows"))
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.stride(0)
+
+
+def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repetition=None, frequency=None,
+                   presence=None, bias_offsets=None, bias_ids=None, bias_values=None, mask=None, mask_rows=None,
+                   out=None, stream=None):
+    """Penalties, biases and a grammar mask on logits (``dsel_logits``).
+
+    ``logits``: [rows, vocab], bfloat16 or float32, any row stride.  ``tokens``: [rows, width]
+    int32 / int64, of which the first ``total_len[r]`` are the row's text and the first
+    ``prompt_len[r]`` its prompt.  ``repetition`` / ``frequency`` / ``presence``: float32, one
+    per row.  ``bias_ids`` (int32) and ``bias_values`` (float32) hold all rows' biases one
+    after another, row r's from ``bias_offsets[r]`` (int32 [rows + 1]) on.  ``mask``: int32
+    [n, words], bit v % 32 of word v // 32 set where token v is allowed; row r uses mask
+    row ``mask_rows[r]`` (int32; -1: not masked), or row r.
+
+    Returns float32 [rows, n], n = vocab rounded up to the TopK row-stride requirement,
+    with -inf in the columns behind the vocabulary.  ``out`` may supply that tensor; it
+    may be ``logits`` itself when that is float32, contiguous and of such a width.
+    """
+    import torch
+
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a 2-D CUDA tensor [rows, vocab] (there is no CPU path)")
+    if logits.dtype == torch.bfloat16:
+        dt = DSEL_BF16
+    elif logits.dtype == torch.float32:
+        dt = DSEL_F32
+    else:
+        raise TypeError("logits must be bfloat16 or float32")
+    dev = logits.device
+    rows, vocab = logits.shape
+    if vocab < 1:
+        raise ValueError("logits must have at least one column")
+    x_stride = _rows_of("logits", logits, dev, None)
+    width = t_stride = 0
+    t_dt = DSEL_I32
+    if tokens is not None:
+        t_dt = _index_dtype("tokens", tokens)
+        t_stride = _rows_of("tokens", tokens, dev, rows)
+        width = tokens.shape[1]
+    elif not (prompt_len is None and total_len is None and repetition is None and frequency is None
+              and presence is None):
+        raise ValueError("penalties and lengths need tokens=")
+    prompt_len = _vector("prompt_len", prompt_len, dev, torch.int32, rows)
+    total_len = _vector("total_len", total_len, dev, torch.int32, rows)
+    repetition = _vector("repetition", repetition, dev, torch.float32, rows)
+    frequency = _vector("frequency", frequency, dev, torch.float32, rows)
+    presence = _vector("presence", presence, dev, torch.float32, rows)
+    if not (bias_offsets is None) == (bias_ids is None) == (bias_values is None):
+        raise ValueError("bias_offsets, bias_ids and bias_values come together")
+    bias_count = 0
+    if bias_ids is not None:
+        bias_ids = _vector("bias_ids", bias_ids, dev, torch.int32, None)
+        bias_count = bias_ids.shape[0]
+        bias_values = _vector("bias_values", bias_values, dev, torch.float32, bias_count)
+        bias_offsets = _vector("bias_offsets", bias_offsets, dev, torch.int32, rows + 1)
+        if bias_count == 0:
+            bias_offsets = bias_ids = bias_values = None
+    m_stride = m_count = 0
+    if mask is not None:
+        if mask.dtype != torch.int32:
+            raise TypeError("mask must be int32 words")
+        m_stride = _rows_of("mask", mask, dev, None)
+        m_count = mask.shape[0]
+        mask_rows = _vector("mask_rows", mask_rows, dev, torch.int32, rows)
+        if mask.shape[1] * 32 < vocab:
+            raise ValueError("mask rows must hold a bit for every token")
+        if mask_rows is None and m_count < rows:
+            raise ValueError("mask needs a row for every row of logits, or mask_rows=")
+        if m_count == 0:
+            mask = mask_rows = None
+    elif mask_rows is not None:
+        raise ValueError("mask_rows needs mask=")
+    if out is not None and (out.dtype != torch.float32 or out.device != dev or out.dim() != 2 or out.shape[0] != rows
+                            or out.shape[1] < vocab or out.shape[1] % 16 or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous float32 tensor [rows, n], n >= vocab a multiple of 16")
+
+    def call(handle):
+        o = out if out is not None else torch.empty((rows, (vocab + 15) // 16 * 16), dtype=torch.float32, device=dev)
+        _check(lib.dsel_logits(logits.data_ptr(), dt, rows, vocab, x_stride, _ptr(tokens), t_dt, width, t_stride,
+                               _ptr(prompt_len), _ptr(total_len), _ptr(repetition), _ptr(frequency), _ptr(presence),
+                               _ptr(bias_offsets), _ptr(bias_ids), _ptr(bias_values), bias_count, _ptr(mask),
+                               m_stride, m_count, _ptr(mask_rows), o.data_ptr(), o.shape[1], handle))
+        return o
+
+    return _run(dev, stream, call)
