@@ -79,6 +79,9 @@ extern "C" {
 /* dtype */
 #define DSEL_BF16 0
 #define DSEL_F32 1
+/* operands of the scores and the attention around the TopK (dsel_topk takes the two above) */
+#define DSEL_F16 2
+#define DSEL_E4M3 3
 /* index_dtype */
 #define DSEL_I32 0
 #define DSEL_I64 1
@@ -349,6 +352,48 @@ DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, 
                          const float* presence, const int32_t* bias_offsets, const int32_t* bias_ids,
                          const float* bias_values, int64_t bias_count, const void* mask, int64_t mask_stride,
                          int64_t mask_count, const int32_t* mask_rows, float* out, int64_t out_stride, void* stream);
+
+/*
+ * Paged caches (dsel_index_score, dsel_sparse_attn).  Key s of sequence b lies in
+ * page table[b][s / page_size], at place s % page_size in it.  A key whose place in
+ * the table is outside it (s / page_size >= table_width) or whose page is outside
+ * [0, pages) does not exist: it scores -inf and takes no part in attention.  Query t
+ * belongs to sequence seq_ids[t] and sees the keys before end[t]; a seq_ids[t]
+ * outside [0, seqs) leaves it none.  seq_ids NULL: query t is of sequence t
+ * (tokens == seqs), or all are of the only one (seqs == 1).  Queries of one sequence
+ * are served fastest next to each other; any order is right.
+ */
+
+/*
+ * dsel_index_score -- the Lightning Indexer's score of every cached key for each
+ * query: the rows dsel_topk selects from.
+ *   score[t][s] = key_scale[s] * sum_h weights[t][h] * max(0, sum_d q[t][h][d] * key[s][d])
+ * for s < end[t]; out[t][s] = -inf for s >= end[t] up to row_stride and for keys that
+ * do not exist, so dsel_topk takes the rows with or without `end`.  Products and sums
+ * in float32, rounded once to out_dtype; a NaN in q or a key gives a NaN score.
+ * A "key" is whatever is to be selected: a token's, or one that stands for a block.
+ *   q            device [tokens][heads][dim] of `dtype` (DSEL_BF16 / _F16 / _E4M3), strides
+ *                in elements; dim a multiple of 32 from 32 to 128, heads 1 to 128
+ *   weights      device float32 [tokens][heads], row stride weights_stride
+ *   keys         device [pages][page_size][dim] of `dtype`, strides in elements (page_size
+ *                any); base, row and page strides of q and keys multiples of 16 bytes
+ *   key_scale    device float32 [pages][page_size], page stride scale_page_stride, or NULL: 1
+ *   table        device int32 [seqs][table_width], row stride table_stride
+ *   seq_ids      device int32 [tokens] or NULL (above)
+ *   end          device int32 [tokens], clamped to [0, row_stride]
+ *   out          device [tokens][row_stride], DSEL_BF16 or DSEL_F32 (out_dtype), 16-byte
+ *                aligned; row_stride a multiple of dsel_stride_requirement().  It may
+ *                share no memory with the inputs.
+ * Returns DSEL_OK, DSEL_ERR_DTYPE / _ROWS / _SHAPE / _STRIDE / _NULL / _ALIGN / _DEVICE or
+ * DSEL_ERR_CUDA.  One launch, asynchronous on `stream`, no workspace; can be captured.
+ */
+DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t heads, int32_t dim,
+                              int64_t q_token_stride, int64_t q_head_stride, const float* weights,
+                              int64_t weights_stride, const void* keys, int32_t pages, int32_t page_size,
+                              int64_t page_stride, int64_t key_stride, const float* key_scale,
+                              int64_t scale_page_stride, const int32_t* table, int32_t seqs, int32_t table_width,
+                              int64_t table_stride, const int32_t* seq_ids, const int32_t* end, void* out,
+                              int out_dtype, int64_t row_stride, void* stream);
 
 /* Row-stride requirement in elements for `dtype` (the pages' get_stride_requirement,
  * narracomm paragraph on install and switches): 16 for both dtypes, so every row

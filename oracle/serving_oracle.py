@@ -59,3 +59,46 @@ def oracle_logits(x, stride, *, tokens=None, prompt_len=None, total_len=None, re
                             z[v], m[v], n[v] = -np.inf, 0.0, 0.0
             y[r, :vocab], mag[r, :vocab], rnd[r, :vocab] = z, m, n
     return y, mag, rnd
+
+
+def _slots(table, seq, page_size, pages, positions):
+    """(page, place) of each position of a sequence; page -1 where it does not exist."""
+    page = np.full(len(positions), -1, dtype=np.int64)
+    if 0 <= seq < table.shape[0]:
+        i = positions // page_size
+        inside = i < table.shape[1]
+        page[inside] = table[seq, i[inside]]
+        page[(page < 0) | (page >= pages)] = -1
+    return page, positions % page_size
+
+
+def _sequence(t, seq_ids, table):
+    return int(seq_ids[t]) if seq_ids is not None else (0 if table.shape[0] == 1 else t)
+
+
+def oracle_score(q, weights, keys, table, end, row_stride, *, seq_ids=None, key_scale=None):
+    """Scores [tokens, row_stride] (float64) and a bound on what float32 sums can be off by.
+
+    The bound: a product of two operands of at most 11 bits is exact; a sum of dim products in
+    float32, whatever its order and with truncated additions, is off by at most
+    (dim + 8) * 2^-23 times the sum of their magnitudes; each head's weighted term and each
+    addition of the sum over heads rounds once (2^-24 of the running magnitude, heads + 8 times)."""
+    tokens, heads, dim = q.shape
+    out = np.full((tokens, row_stride), -np.inf)
+    err = np.zeros((tokens, row_stride))
+    with np.errstate(invalid="ignore", over="ignore"):
+        for t in range(tokens):
+            n = min(max(int(end[t]), 0), row_stride)
+            pos = np.arange(n)
+            page, place = _slots(table, _sequence(t, seq_ids, table), keys.shape[1], keys.shape[0], pos)
+            pos, page, place = pos[page >= 0], page[page >= 0], place[page >= 0]
+            k = keys[page, place].astype(np.float64)
+            z = q[t].astype(np.float64) @ k.T
+            a = np.abs(q[t].astype(np.float64)) @ np.abs(k).T
+            w = weights[t].astype(np.float64)[:, None]
+            z = np.where(np.isnan(z), z, np.maximum(z, 0))
+            s = key_scale[page, place].astype(np.float64) if key_scale is not None else np.ones(len(pos))
+            out[t, pos] = (w * z).sum(0) * s
+            err[t, pos] = ((np.abs(w) * a).sum(0) * (dim + 8) * 2.0 ** -23
+                           + (np.abs(w) * z).sum(0) * (heads + 8) * 2.0 ** -24) * np.abs(s) + 2.0 ** -120
+    return out, err

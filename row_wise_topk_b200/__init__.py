@@ -20,7 +20,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, os.path.basename(os.environ.get("ROW_WISE_TOPK_LIB", "libdsel.so")))
 
 # Constants of include/dsel.h
-DSEL_BF16, DSEL_F32 = 0, 1
+DSEL_BF16, DSEL_F32, DSEL_F16, DSEL_E4M3 = 0, 1, 2, 3
 DSEL_I32, DSEL_I64 = 0, 1
 DSEL_NAN_TRAP, DSEL_NAN_FLAG = 0, 1
 DSEL_ORDER_NONE, DSEL_ORDER_INDEX, DSEL_ORDER_VALUE = 0, 1, 2
@@ -81,6 +81,9 @@ def _load() -> ctypes.CDLL:
     lib.dsel_logits.restype = c_int
     lib.dsel_logits.argtypes = [vp, c_int, c_i64, i32, c_i64, vp, c_int, i32, c_i64, vp, vp, vp, vp, vp, vp, vp, vp,
                                 c_i64, vp, c_i64, c_i64, vp, vp, c_i64, vp]
+    lib.dsel_index_score.restype = c_int
+    lib.dsel_index_score.argtypes = [vp, c_int, c_i64, i32, i32, c_i64, c_i64, vp, c_i64, vp, i32, i32, c_i64, c_i64,
+                                     vp, c_i64, vp, i32, i32, c_i64, vp, vp, vp, c_int, c_i64, vp]
     lib.dsel_stride_requirement.restype = c_i64
     lib.dsel_stride_requirement.argtypes = [c_int]
     lib.dsel_status_string.restype = ctypes.c_char_p
@@ -305,4 +308,4 @@ def topk_sample(logits, k: int, u, *, temperature: float = 1.0, top_p: float = 1
 
 
 # the operators before and after the selection (same manner: torch tensors in, one library call)
-from .serving import process_logits  # noqa: E402,F401
+from .serving import index_score, process_logits  # noqa: E402,F401

@@ -6,6 +6,7 @@
 
 #include "../../include/dsel.h"
 #include "dsel_kernels.cuh"
+#include "dsel_ops.cuh"
 #include "dsel_plan.h"
 #include "dsel_resident.cuh"
 #include "dsel_slice.cuh"
@@ -626,13 +627,14 @@ DSEL_API int dsel_topk_noalloc(const void* x, int dtype, int64_t rows, int64_t r
 
 DSEL_API int dsel_device_status(int* status_out, void* stream) {
   if (status_out == nullptr) return DSEL_ERR_NULL;
-  int v = 0, zero = 0;
+  int v = 0, score = 0, zero = 0;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (score_status(&score, cs) != DSEL_OK) return DSEL_ERR_CUDA;
   if (cudaMemcpyFromSymbolAsync(&v, g_device_status, sizeof(int), 0, cudaMemcpyDeviceToHost, cs) != cudaSuccess ||
       cudaMemcpyToSymbolAsync(g_device_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, cs) != cudaSuccess ||
       cudaStreamSynchronize(cs) != cudaSuccess)
     return DSEL_ERR_CUDA;
-  *status_out = v;
+  *status_out = v != 0 ? v : score;
   return DSEL_OK;
 }
 

@@ -62,11 +62,29 @@ inline bool ranges_meet(const void* a, int64_t na, int ea, const void* b, int64_
   return pa < pb + uintptr_t(nb) * uintptr_t(eb) && pb < pa + uintptr_t(na) * uintptr_t(ea);
 }
 
+// Reads and clears the status word of the score kernel's bounded waits (asynchronous on `st`).
+int score_status(int* out, cudaStream_t st);
+
 // ---- device ----
 
 // The launches before this one in the stream are complete and visible.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The next launch may start its set-up.
 __device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t shared_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// 16 bytes global -> shared, asynchronous; zeros where !live (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N groups of this thread are complete.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 }  // namespace dsel

@@ -1,0 +1,683 @@
+// dsel_index_score: the Lightning Indexer's score of every cached key for each
+// query, the rows that dsel_topk selects from.
+//
+//   score[t][s] = scale[s] * sum_h weights[t][h] * max(0, q[t][h] . key[s])   for s < end[t], else -inf
+//
+// A product of key tiles with query heads, so it runs on the tensor cores: the 128
+// keys of a tile are the rows of D (one TMEM lane each), the heads of one or more
+// queries its columns (one f32 column each), the head dimension is the depth.  With
+// the heads in columns, the weighted sum over heads is a loop over the registers of
+// the thread that owns a key: no shuffle, and its scores leave as coalesced rows.
+//
+// What bounds it: one query per sequence (decoding) reads 2 * dim bytes of key for
+// 2 * heads * dim operations: HBM.  A chunk of queries over the same keys is bound by
+// the tensor cores (2 * heads * dim operations per score), beside which the sum over
+// heads costs 1.75 issue slots per (key, head): the epilogue of one accumulator runs
+// under the products of the other.
+//
+// Roles of a persistent CTA: 8 warps read accumulators, sum over heads and store
+// (warpgroup b owns accumulator b), 4 warps bring key tiles and queries with 16-byte
+// asynchronous copies (pages may end anywhere, so each key is addressed through the
+// page table by itself; a tensor-map box would need pages of a fixed power of two),
+// one warp issues the products.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "dsel_ops.cuh"
+
+namespace dsel {
+
+namespace {
+
+__device__ int g_score_status;   // DSEL_ERR_DEVICE_TIMEOUT when a wait gave up
+
+constexpr int kTile = 128;            // keys per tile (TMEM lanes)
+constexpr int kPanel = kTile * 128;   // a tile's panel: 128 rows of 128 bytes, 128-byte swizzle
+constexpr int kEpiWarps = 8;
+constexpr int kProdWarps = 4;
+constexpr int kProdThreads = kProdWarps * 32;
+constexpr int kScThreads = (kEpiWarps + kProdWarps + 1) * 32;
+constexpr int kMaxRing = 8;
+constexpr int kScoreSmem = 227 * 1024;   // all of a CTA's shared memory
+constexpr int kBarBytes = 256;          // the barriers and the accumulators' address
+constexpr uint64_t kWaitLimit = 2000000000ull;   // 2 s
+
+struct ScoreParams {
+  const uint8_t* q;
+  int64_t q_token_bytes, q_head_bytes;
+  const float* weights;
+  int64_t weights_stride;
+  const uint8_t* keys;
+  int64_t page_bytes, key_bytes;
+  const float* key_scale;
+  int64_t scale_page_stride;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* seq_ids;
+  const int32_t* end;
+  void* out;
+  int64_t row_stride;
+  int32_t pages, page_size, page_shift;   // page_shift >= 0: page_size is 1 << page_shift
+  int32_t seqs, table_width;
+  int32_t tokens, heads, row_bytes;       // row_bytes: dim * element size
+  int32_t col_tiles;                      // accumulators per key tile: 1 or 2
+  int32_t ring, lag;                      // key tiles in shared memory; copies in flight before the oldest is awaited
+  int32_t q_bufs;                         // query buffers
+  int32_t chunk;                          // key tiles per work item
+  int32_t chunks, items;
+  int32_t seq_mode;                       // 0: seq_ids, 1: token t is sequence t, 2: one sequence
+  int32_t out_f32;
+};
+
+// ---- PTX ----
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+// Bounded wait: false (and a device status) after two seconds.
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = now_ns();
+  while (!bar_try(bar, parity)) {
+    if (now_ns() - t0 > kWaitLimit) {
+      atomicExch(&g_score_status, DSEL_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  return bar_try(bar, parity) || bar_wait_slow(bar, parity);
+}
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Shared-memory descriptor of a K-major operand in 128-byte-swizzled panels: address,
+// 1024 bytes between groups of 8 rows, descriptor version 1, swizzle mode 2 (128 bytes).
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+template <bool kByte>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  const uint32_t acc = accumulate ? 1u : 0u;
+  if (kByte)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float relu(float x) {   // a NaN stays one
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(uint64_t a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+  return x + y;
+}
+
+// A work item: up to 32 consecutive queries (one per lane) and a range of key tiles.
+// Queries of one sequence that follow each other share its key tiles: a run.
+struct Item {
+  int32_t token0, count;   // queries of the item
+  int32_t seq, end;        // this lane's query: its sequence (-1: none) and its visible keys
+  uint32_t starts;         // bit i: lane i starts a run
+  int32_t tile0;           // first key tile
+};
+
+__device__ __forceinline__ Item load_item(const ScoreParams& p, int32_t item, int per_item) {
+  Item it;
+  const int lane = int(threadIdx.x & 31);
+  const int32_t group = item / p.chunks;
+  it.tile0 = (item - group * p.chunks) * p.chunk;
+  it.token0 = group * per_item;
+  it.count = p.tokens - it.token0 < per_item ? p.tokens - it.token0 : per_item;
+  const int32_t t = it.token0 + lane;
+  it.seq = -1;
+  it.end = 0;
+  if (lane < it.count) {
+    it.seq = p.seq_mode == 0 ? p.seq_ids[t] : (p.seq_mode == 1 ? t : 0);
+    if (it.seq < 0 || it.seq >= p.seqs) it.seq = -1;
+    it.end = p.end[t];
+    it.end = it.end < 0 ? 0 : (it.end > p.row_stride ? int32_t(p.row_stride) : it.end);
+    if (it.seq < 0) it.end = 0;
+  }
+  const int32_t before = __shfl_up_sync(0xFFFFFFFFu, it.seq, 1);
+  it.starts = __ballot_sync(0xFFFFFFFFu, lane < it.count && (lane == 0 || before != it.seq));
+  return it;
+}
+
+// The run that starts at lane a: its end lane, its sequence, the key tiles of this item that any of its queries sees.
+struct Run {
+  int a, b;
+  int32_t seq, end, tiles;
+};
+
+__device__ __forceinline__ Run load_run(const ScoreParams& p, const Item& it, int a) {
+  Run r;
+  const int lane = int(threadIdx.x & 31);
+  const uint32_t later = a < 31 ? it.starts & ~((2u << a) - 1u) : 0u;
+  r.a = a;
+  r.b = later != 0u ? __ffs(later) - 1 : it.count;
+  r.seq = __shfl_sync(0xFFFFFFFFu, it.seq, a);
+  r.end = __reduce_max_sync(0xFFFFFFFFu, lane >= a && lane < r.b ? it.end : 0);
+  const int32_t n = (r.end + kTile - 1) / kTile - it.tile0;
+  r.tiles = n < 0 ? 0 : (n > p.chunk ? p.chunk : n);
+  return r;
+}
+
+__device__ __forceinline__ int64_t key_slot(const ScoreParams& p, const int32_t* table, int32_t pos, int32_t* page_out) {
+  const int32_t i = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
+  int32_t page = -1;
+  if (i < p.table_width) page = table[i];
+  if (page < 0 || page >= p.pages) page = -1;
+  *page_out = page;
+  return pos - i * p.page_size;
+}
+
+// kByte: e4m3 operands.  kHeads: heads per query, padded.  kCols: columns of an accumulator.
+template <bool kByte, int kHeads, int kCols>
+__global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_constant__ ScoreParams p,
+                                                             const uint32_t idesc) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int kPerTile = kCols / kHeads;   // queries of an accumulator
+  const uint32_t ring0 = shared_addr(smem);
+  const int panels = (p.row_bytes + 127) / 128;
+  const uint32_t stage_bytes = uint32_t(panels) * kPanel;
+  const uint32_t q0 = ring0 + uint32_t(p.ring) * stage_bytes;
+  const uint32_t q_panel = uint32_t(kCols) * 128u;                       // one accumulator's queries, one panel
+  const uint32_t q_bytes = uint32_t(p.col_tiles * panels) * q_panel;     // one query buffer
+  uint8_t* tail = smem + p.ring * stage_bytes + p.q_bufs * q_bytes;
+  float* wsm = reinterpret_cast<float*>(tail);                           // [2][kCols] weights
+  const uint32_t full0 = shared_addr(tail + 2 * kCols * 4), empty0 = full0 + 8 * kMaxRing;
+  const uint32_t done0 = full0 + 16 * kMaxRing, free0 = done0 + 16, qfree0 = free0 + 16;
+  const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+  const int per_item = kPerTile * p.col_tiles;
+  static_assert((2 * kMaxRing + 6) * 8 + 8 <= kBarBytes, "barriers outgrew their reservation");
+  uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(tail + 2 * kCols * 4 + (2 * kMaxRing + 6) * 8);
+  if ((ring0 & 1023u) != 0u) {   // the swizzled panels need it; the dynamic window starts aligned when it is alone
+    if (threadIdx.x == 0) atomicExch(&g_score_status, DSEL_ERR_ALIGN);
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.ring; ++i) {
+      bar_init(full0 + 8 * i, kProdThreads);
+      bar_init(empty0 + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(done0 + 8 * i, 1);
+      bar_init(free0 + 8 * i, 128);
+      bar_init(qfree0 + 8 * i, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  constexpr uint32_t kTmemCols = 2 * kCols < 32 ? 32 : 2 * kCols;
+  if (warp == kEpiWarps + kProdWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_addr(tmem_base_sh)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base_sh;
+  grid_wait();
+  grid_launch();
+
+  if (warp < kEpiWarps) {
+    // ---------------- sum over heads, stores ----------------
+    const int b = warp >> 2;                       // warpgroup and accumulator
+    const int row = int(threadIdx.x & 127);        // key of the tile
+    const uint32_t acc = tmem + uint32_t(b * kCols) + (uint32_t(warp & 3) << 21);   // lane quarter in bits 16..
+    float* w = wsm + b * kCols;
+    uint32_t uses = 0;    // times this accumulator was filled
+    uint32_t turn = 0;    // key tiles so far (col_tiles == 1: accumulators take turns)
+    bool ok = true;
+    // (a wait that gave up ends the work, not the loop: every warp passes the same barriers)
+    for (int32_t item = int32_t(blockIdx.x); item < p.items; item += int32_t(gridDim.x)) {
+      const Item it = load_item(p, item, per_item);
+      const int first = p.col_tiles == 2 ? b * kPerTile : 0;   // the queries of this warpgroup's columns
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + b) : "memory");   // the last item's weights are no longer read
+      for (int i = row; i < kCols; i += 128) {
+        const int qi = first + i / kHeads, h = i % kHeads;
+        w[i] = qi < it.count && h < p.heads ? p.weights[int64_t(it.token0 + qi) * p.weights_stride + h] : 0.f;
+      }
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + b) : "memory");
+      const int64_t pos0 = int64_t(it.tile0) * kTile;
+      const int64_t pos_end = pos0 + int64_t(p.chunk) * kTile < p.row_stride ? pos0 + int64_t(p.chunk) * kTile : p.row_stride;
+      for (int a = 0; a < it.count && ok;) {
+        const Run run = load_run(p, it, a);
+        a = run.b;
+        // queries of this warpgroup's columns in the run
+        const int lo = run.a > first ? run.a : first;
+        const int hi = run.b < first + kPerTile ? run.b : first + kPerTile;
+        const int32_t* table = p.table + int64_t(run.seq < 0 ? 0 : run.seq) * p.table_stride;
+        for (int32_t k = 0; k < run.tiles; ++k) {
+          const bool mine = p.col_tiles == 2 ? lo < hi : int(turn & 1u) == b;
+          ++turn;
+          if (!mine) continue;
+          // the key's page and scale, while the product runs
+          const int32_t pos = (it.tile0 + k) * kTile + row;
+          bool live = pos < run.end;
+          float scale = 1.f;
+          if (live) {
+            int32_t page;
+            const int64_t at = key_slot(p, table, pos, &page);
+            live = page >= 0;
+            if (live && p.key_scale != nullptr) scale = p.key_scale[int64_t(page) * p.scale_page_stride + at];
+          }
+          if (!bar_wait(done0 + 8 * b, uses & 1u)) {
+            ok = false;
+            break;
+          }
+          ++uses;
+          tc_fence_after();
+          for (int qi = lo; qi < hi; ++qi) {
+            const int c0 = (qi - first) * kHeads;
+            uint64_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;   // four pairs of sums, to shorten the chains
+#pragma unroll
+            for (int c = 0; c < kHeads; c += 16) {
+              uint32_t x[16];
+              tmem_load16(acc + uint32_t(c0 + c), x);
+              tmem_wait();
+              if (c < p.heads) {
+                if (c + 16 > p.heads) {   // columns behind the last head count for nothing, whatever they hold
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    if (c + i >= p.heads) x[i] = 0u;
+                }
+                const ulonglong2* w2 = reinterpret_cast<const ulonglong2*>(w + c0 + c);
+#pragma unroll
+                for (int i = 0; i < 16; i += 8) {
+                  const ulonglong2 wa = w2[i / 4], wb = w2[i / 4 + 1];
+                  s0 = fma2(pack2(relu(__uint_as_float(x[i + 0])), relu(__uint_as_float(x[i + 1]))), wa.x, s0);
+                  s1 = fma2(pack2(relu(__uint_as_float(x[i + 2])), relu(__uint_as_float(x[i + 3]))), wa.y, s1);
+                  s2 = fma2(pack2(relu(__uint_as_float(x[i + 4])), relu(__uint_as_float(x[i + 5]))), wb.x, s2);
+                  s3 = fma2(pack2(relu(__uint_as_float(x[i + 6])), relu(__uint_as_float(x[i + 7]))), wb.y, s3);
+                }
+              }
+            }
+            const int32_t end = __shfl_sync(0xFFFFFFFFu, it.end, qi);
+            float v = ((sum2(s0) + sum2(s1)) + (sum2(s2) + sum2(s3))) * scale;
+            if (!live || pos >= end) v = -__int_as_float(0x7F800000);
+            if (pos < p.row_stride) {
+              const int64_t o = int64_t(it.token0 + qi) * p.row_stride + pos;
+              if (p.out_f32)
+                static_cast<float*>(p.out)[o] = v;
+              else
+                static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+            }
+          }
+          tc_fence_before();
+          bar_arrive(free0 + 8 * b);
+        }
+        // -inf behind the run's last tile (both warpgroups' threads, 16 bytes each)
+        const int64_t from = pos0 + int64_t(run.tiles) * kTile;
+        const int step = p.out_f32 ? 4 : 8;
+        const uint32_t fill = p.out_f32 ? 0xFF800000u : 0xFF80FF80u;
+        for (int qi = run.a; qi < run.b; ++qi)
+          for (int64_t pos = from + int64_t(threadIdx.x) * step; pos < pos_end; pos += kEpiWarps * 32 * step) {
+            const int64_t o = (int64_t(it.token0 + qi) * p.row_stride + pos) * (p.out_f32 ? 4 : 2);
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + o) = make_uint4(fill, fill, fill, fill);
+          }
+      }
+    }
+  } else if (warp < kEpiWarps + kProdWarps) {
+    // ---------------- key tiles and queries ----------------
+    const int pw = warp - kEpiWarps;
+    const int tid = pw * 32 + lane;
+    const int per_row = p.row_bytes / 16;   // 16-byte pieces of a key
+    uint32_t issued = 0, told = 0;          // tiles whose copies were started; tiles announced as complete
+    uint32_t n_item = 0;                    // items that had a tile
+    bool ok = true;
+    auto tell = [&]() {   // announce the oldest tile that is not yet: its copies are complete, and visible to the products
+      fence_async_shared();
+      bar_arrive(full0 + 8 * (told % uint32_t(p.ring)));
+      ++told;
+    };
+    auto flush = [&]() {
+      copy_wait<0>();
+      while (told < issued) tell();
+    };
+    for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
+      const Item it = load_item(p, item, per_item);
+      bool queries = false;   // loaded for this item
+      for (int a = 0; a < it.count && ok;) {
+        const Run run = load_run(p, it, a);
+        a = run.b;
+        const int32_t* table = p.table + int64_t(run.seq < 0 ? 0 : run.seq) * p.table_stride;
+        for (int32_t k = 0; k < run.tiles; ++k) {
+          // this thread's key of the tile: where it lies
+          const int32_t pos = (it.tile0 + k) * kTile + tid;
+          int64_t off = -1;
+          if (pos < run.end) {
+            int32_t page;
+            const int64_t at = key_slot(p, table, pos, &page);
+            if (page >= 0) off = int64_t(page) * p.page_bytes + at * p.key_bytes;
+          }
+          if (!queries) {
+            const uint32_t buf = n_item % uint32_t(p.q_bufs), use = n_item / uint32_t(p.q_bufs);
+            if (use > 0) {
+              // the products that read this buffer may still wait for tiles not yet announced
+              if (!bar_try(qfree0 + 8 * buf, (use - 1) & 1u)) flush();
+              if (!bar_wait(qfree0 + 8 * buf, (use - 1) & 1u)) {
+                ok = false;
+                break;
+              }
+            }
+            const uint32_t qb = q0 + buf * q_bytes;
+            const int rows = p.col_tiles * kCols;
+            for (int i = tid; i < rows * per_row; i += kProdThreads) {
+              const int r = i / per_row, piece = i - r * per_row;
+              const int qi = r / kHeads, h = r % kHeads;
+              const bool in = qi < it.count && h < p.heads;
+              const uint8_t* src = p.q;
+              if (in) src += int64_t(it.token0 + qi) * p.q_token_bytes + int64_t(h) * p.q_head_bytes + piece * 16;
+              const int ct = r / kCols, rr = r % kCols;
+              const uint32_t dst = qb + uint32_t(ct * panels + (piece >> 3)) * q_panel + uint32_t(rr) * 128u +
+                                   (uint32_t((piece & 7) ^ (rr & 7)) << 4);
+              copy16(dst, src, in);
+            }
+            queries = true;
+            ++n_item;
+          }
+          const uint32_t slot = issued % uint32_t(p.ring), round = issued / uint32_t(p.ring);
+          if (round > 0 && !bar_wait(empty0 + 8 * slot, (round - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst0 = ring0 + slot * stage_bytes;
+          // each warp brings its own 32 keys, consecutive lanes consecutive pieces
+          for (int i = lane; i < 32 * per_row; i += 32) {
+            const int r = i / per_row, piece = i - r * per_row;
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+            const int rr = pw * 32 + r;
+            const uint32_t dst = dst0 + uint32_t(piece >> 3) * kPanel + uint32_t(rr) * 128u +
+                                 (uint32_t((piece & 7) ^ (rr & 7)) << 4);
+            copy16(dst, p.keys + (o < 0 ? 0 : o + piece * 16), o >= 0);
+          }
+          copy_commit();
+          ++issued;
+          if (int32_t(issued - told) > p.lag) {
+            if (p.lag >= 4)
+              copy_wait<4>();
+            else if (p.lag == 3)
+              copy_wait<3>();
+            else if (p.lag == 2)
+              copy_wait<2>();
+            else
+              copy_wait<1>();
+            tell();
+          }
+        }
+      }
+    }
+    flush();   // also on the way out after a wait that gave up: no copy stays in flight
+  } else {
+    // ---------------- products ----------------
+    uint32_t taken = 0;          // key tiles
+    uint32_t uses[2] = {0, 0};   // accumulators filled
+    uint32_t n_item = 0;
+    uint32_t turn = 0;
+    bool ok = true;
+    const int steps = p.row_bytes / 32;
+    for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
+      const Item it = load_item(p, item, per_item);
+      bool any = false;
+      for (int a = 0; a < it.count && ok;) {
+        const Run run = load_run(p, it, a);
+        a = run.b;
+        for (int32_t k = 0; k < run.tiles && ok; ++k) {
+          any = true;
+          const uint32_t slot = taken % uint32_t(p.ring);
+          if (!bar_wait(full0 + 8 * slot, (taken / uint32_t(p.ring)) & 1u)) {
+            ok = false;
+            break;
+          }
+          const uint32_t qb = q0 + (n_item % uint32_t(p.q_bufs)) * q_bytes;
+          for (int n = 0; n < p.col_tiles; ++n) {
+            const int b = p.col_tiles == 2 ? n : int(turn & 1u);
+            if (p.col_tiles == 2 && (run.b <= n * kPerTile || run.a >= (n + 1) * kPerTile)) continue;   // no query of it
+            if (uses[b] > 0 && !bar_wait(free0 + 8 * b, (uses[b] - 1) & 1u)) {
+              ok = false;
+              break;
+            }
+            ++uses[b];
+            tc_fence_after();
+            if (lane == 0) {   // always the same thread: a commit covers its own products
+              for (int s = 0; s < steps; ++s) {
+                const uint32_t in = uint32_t(s & 3) * 32u;
+                mma<kByte>(tmem + uint32_t(b * kCols),
+                           operand(ring0 + slot * stage_bytes + uint32_t(s >> 2) * kPanel + in),
+                           operand(qb + uint32_t(n * panels + (s >> 2)) * q_panel + in), idesc, s > 0);
+              }
+              tc_commit(done0 + 8 * b);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (lane == 0) tc_commit(empty0 + 8 * slot);
+          __syncwarp();
+          ++taken;
+          ++turn;
+        }
+      }
+      if (any) {
+        if (ok && lane == 0) tc_commit(qfree0 + 8 * (n_item % uint32_t(p.q_bufs)));
+        __syncwarp();
+        ++n_item;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kEpiWarps + kProdWarps) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+template <bool kByte, int kHeads, int kCols>
+int launch_score(const ScoreParams& p, int dtype, int grid, int smem, cudaStream_t st) {
+  auto kern = score_kernel<kByte, kHeads, kCols>;
+  if (allow_smem(reinterpret_cast<const void*>(kern), kScoreSmem) != cudaSuccess) return DSEL_ERR_CUDA;
+  // D f32, A and B of the operands' type (f16 0, bf16 1; e4m3 0), both K-major, N / 8, M / 16
+  const uint32_t type = dtype == DSEL_BF16 ? 1u : 0u;
+  const uint32_t idesc =
+      (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kCols / 8) << 17) | (uint32_t(kTile / 16) << 24);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid), 1, 1);
+  cfg.blockDim = dim3(kScThreads, 1, 1);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, idesc) == cudaSuccess ? DSEL_OK : DSEL_ERR_CUDA;
+}
+
+template <bool kByte>
+int launch_heads(const ScoreParams& p, int dtype, int hp, bool wide, int grid, int smem, cudaStream_t st) {
+  if (hp == 16)
+    return wide ? launch_score<kByte, 16, 256>(p, dtype, grid, smem, st)
+                : launch_score<kByte, 16, 16>(p, dtype, grid, smem, st);
+  if (hp == 32)
+    return wide ? launch_score<kByte, 32, 256>(p, dtype, grid, smem, st)
+                : launch_score<kByte, 32, 32>(p, dtype, grid, smem, st);
+  if (hp == 64)
+    return wide ? launch_score<kByte, 64, 256>(p, dtype, grid, smem, st)
+                : launch_score<kByte, 64, 64>(p, dtype, grid, smem, st);
+  return wide ? launch_score<kByte, 128, 256>(p, dtype, grid, smem, st)
+              : launch_score<kByte, 128, 128>(p, dtype, grid, smem, st);
+}
+
+}  // namespace
+
+int score_status(int* out, cudaStream_t st) {
+  int zero = 0;
+  if (cudaMemcpyFromSymbolAsync(out, g_score_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaMemcpyToSymbolAsync(g_score_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st) != cudaSuccess)
+    return DSEL_ERR_CUDA;
+  return DSEL_OK;
+}
+
+}  // namespace dsel
+
+using namespace dsel;
+
+DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t heads, int32_t dim,
+                              int64_t q_token_stride, int64_t q_head_stride, const float* weights,
+                              int64_t weights_stride, const void* keys, int32_t pages, int32_t page_size,
+                              int64_t page_stride, int64_t key_stride, const float* key_scale,
+                              int64_t scale_page_stride, const int32_t* table, int32_t seqs, int32_t table_width,
+                              int64_t table_stride, const int32_t* seq_ids, const int32_t* end, void* out,
+                              int out_dtype, int64_t row_stride, void* stream) {
+  if (dtype != DSEL_BF16 && dtype != DSEL_F16 && dtype != DSEL_E4M3) return DSEL_ERR_DTYPE;
+  if (out_dtype != DSEL_BF16 && out_dtype != DSEL_F32) return DSEL_ERR_DTYPE;
+  if (tokens < 0 || tokens > INT32_MAX / 2) return DSEL_ERR_ROWS;
+  const int eb = dtype == DSEL_E4M3 ? 1 : 2;
+  if (heads < 1 || heads > 128 || dim < 32 || dim > 128 || dim % 32 != 0) return DSEL_ERR_SHAPE;
+  if (pages < 0 || page_size < 1 || seqs < 0 || table_width < 0) return DSEL_ERR_SHAPE;
+  if (seq_ids == nullptr && seqs != 1 && int64_t(seqs) != tokens) return DSEL_ERR_SHAPE;
+  if (row_stride < 1 || row_stride % kStrideReq != 0 || row_stride > INT32_MAX - 64 * kTile) return DSEL_ERR_STRIDE;
+  if (q_head_stride < dim || q_token_stride < 0 || weights_stride < heads || key_stride < dim || page_stride < 0 ||
+      table_stride < table_width || scale_page_stride < 0)
+    return DSEL_ERR_STRIDE;
+  // rows of operands are copied in 16-byte pieces
+  if (q_head_stride * eb % 16 != 0 || q_token_stride * eb % 16 != 0 || key_stride * eb % 16 != 0 ||
+      page_stride * eb % 16 != 0)
+    return DSEL_ERR_STRIDE;
+  if (tokens == 0) return DSEL_OK;
+  if (q == nullptr || weights == nullptr || keys == nullptr || table == nullptr || end == nullptr || out == nullptr)
+    return DSEL_ERR_NULL;
+  if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(keys) | reinterpret_cast<uintptr_t>(out)) & 15u) != 0)
+    return DSEL_ERR_ALIGN;
+  if (const int st = check_device(); st != DSEL_OK) return st;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DSEL_ERR_CUDA;
+
+  ScoreParams p = {};
+  p.q = static_cast<const uint8_t*>(q);
+  p.q_token_bytes = q_token_stride * eb;
+  p.q_head_bytes = q_head_stride * eb;
+  p.weights = weights;
+  p.weights_stride = weights_stride;
+  p.keys = static_cast<const uint8_t*>(keys);
+  p.page_bytes = page_stride * eb;
+  p.key_bytes = key_stride * eb;
+  p.key_scale = key_scale;
+  p.scale_page_stride = scale_page_stride;
+  p.table = table;
+  p.table_stride = table_stride;
+  p.seq_ids = seq_ids;
+  p.end = end;
+  p.out = out;
+  p.row_stride = row_stride;
+  p.pages = pages;
+  p.page_size = page_size;
+  p.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if ((int64_t(1) << s) == page_size) p.page_shift = s;
+  p.seqs = seqs;
+  p.table_width = table_width;
+  p.tokens = int32_t(tokens);
+  p.heads = heads;
+  p.row_bytes = dim * eb;
+  p.seq_mode = seq_ids != nullptr ? 0 : (seqs == 1 ? 2 : 1);
+  p.out_f32 = out_dtype == DSEL_F32;
+
+  // One query an accumulator where each sequence has one (decoding: bound by the keys' bytes, so a narrow
+  // accumulator and a deep ring); else as many as 256 columns hold, and two accumulators per key tile
+  // when a sequence has more queries than one holds: each tile then serves twice the queries.
+  const int hp = heads <= 16 ? 16 : heads <= 32 ? 32 : heads <= 64 ? 64 : 128;
+  const int64_t per_seq = seqs > 0 ? (tokens + seqs - 1) / seqs : 1;
+  const bool wide = per_seq > 1;
+  const int cols = wide ? 256 : hp;
+  p.col_tiles = wide && per_seq > 256 / hp ? 2 : 1;
+  const int stage = (p.row_bytes + 127) / 128 * kPanel;
+  const int qbytes = p.col_tiles * ((p.row_bytes + 127) / 128) * cols * 128;
+  const int room = kScoreSmem - kBarBytes - 2 * cols * 4;
+  p.q_bufs = (room - 2 * qbytes) / stage >= 4 ? 2 : 1;
+  p.ring = (room - p.q_bufs * qbytes) / stage;
+  if (p.ring > kMaxRing) p.ring = kMaxRing;
+  p.lag = p.ring - 2 > 4 ? 4 : p.ring - 2;
+  const int smem = p.ring * stage + p.q_bufs * qbytes + 2 * cols * 4 + kBarBytes;
+
+  // Key tiles per work item: the count whose items fill whole rounds of the SMs best, an item's own
+  // cost (its queries) counted as one tile of a narrow accumulator, two of a wide one.
+  const int64_t per_item = int64_t(cols / hp) * p.col_tiles;
+  const int64_t groups = (tokens + per_item - 1) / per_item;
+  const int64_t tiles = (row_stride + kTile - 1) / kTile;
+  const int most = p.col_tiles == 2 ? 64 : 16;
+  int64_t best = -1;
+  for (int c = 1; c <= most && c <= tiles; ++c) {
+    const int64_t items = groups * ((tiles + c - 1) / c);
+    if (items > INT32_MAX / 2) continue;
+    const int64_t cost = (items + sms - 1) / sms * (c + (wide ? 2 : 1));
+    if (best < 0 || cost <= best) {
+      best = cost;
+      p.chunk = c;
+    }
+  }
+  if (best < 0) return DSEL_ERR_ROWS;
+  p.chunks = int32_t((tiles + p.chunk - 1) / p.chunk);
+  p.items = int32_t(groups * p.chunks);
+  const int grid = p.items < sms ? p.items : sms;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return dtype == DSEL_E4M3 ? launch_heads<true>(p, dtype, hp, wide, grid, smem, cs)
+                            : launch_heads<false>(p, dtype, hp, wide, grid, smem, cs);
+}

@@ -1,7 +1,9 @@
 """The operators before and after the TopK of a serving step, over torch tensors.
 
-``process_logits`` makes the rows that ``topk_sample`` (or ``topk``) takes: penalties
-for repeated tokens, biases, a grammar mask.
+- ``process_logits`` makes the rows that ``topk_sample`` (or ``topk``) takes: penalties
+  for repeated tokens, biases, a grammar mask.
+- ``index_score`` makes the rows that ``topk`` selects keys from: the Lightning Indexer's
+  score of every cached key for each query.
 
 Each is one call of the C ABI (``include/dsel.h`` states the formulas and the argument
 rules); this module checks the tensors and allocates the outputs.  Calls run on the
@@ -11,7 +13,7 @@ launch: ``TypeError`` / ``ValueError`` here, ``DselError`` from the library.
 """
 from __future__ import annotations
 
-from . import DSEL_BF16, DSEL_F32, DSEL_I32, DSEL_I64, DSEL_OK, DselError, lib
+from . import (DSEL_BF16, DSEL_E4M3, DSEL_F16, DSEL_F32, DSEL_I32, DSEL_I64, DSEL_OK, DselError, lib)
 
 def _run(device, stream, call):
     """``call(stream handle)`` with `device` current and, for a given stream, as torch's current one."""
@@ -151,6 +153,96 @@ def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repe
                                _ptr(prompt_len), _ptr(total_len), _ptr(repetition), _ptr(frequency), _ptr(presence),
                                _ptr(bias_offsets), _ptr(bias_ids), _ptr(bias_values), bias_count, _ptr(mask),
                                m_stride, m_count, _ptr(mask_rows), o.data_ptr(), o.shape[1], handle))
+        return o
+
+    return _run(dev, stream, call)
+
+
+def _operand_dtype(name, t, byte):
+    """The DSEL code of a 16-bit operand (or, where `byte`, of an e4m3 one)."""
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return DSEL_BF16
+    if t.dtype == torch.float16:
+        return DSEL_F16
+    if byte and t.dtype == torch.float8_e4m3fn:
+        return DSEL_E4M3
+    raise TypeError(f"{name} must be bfloat16" + (", float16 or float8_e4m3fn" if byte else " or float16"))
+
+
+def _queries(q, table, end, seq_ids):
+    """Checks what every query of a paged cache comes with; (device, tokens, table stride)."""
+    import torch
+
+    if q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a 3-D CUDA tensor [tokens, heads, dim] (there is no CPU path)")
+    dev, tokens = q.device, q.shape[0]
+    if q.stride(2) != 1 and q.shape[2] > 1:
+        raise ValueError("q must be contiguous in its last dimension")
+    if table.dtype != torch.int32:
+        raise TypeError("block_table must be int32")
+    t_stride = _rows_of("block_table", table, dev, None)
+    _vector("end", end, dev, torch.int32, tokens)
+    if seq_ids is not None:
+        _vector("seq_ids", seq_ids, dev, torch.int32, tokens)
+    elif table.shape[0] not in (1, tokens):
+        raise ValueError("block_table needs one row, or one for each query, or seq_ids=")
+    return dev, tokens, t_stride
+
+
+def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=None, row_stride=None, out_dtype=None,
+                out=None, stream=None):
+    """Scores of every cached key for each query (``dsel_index_score``), the rows of ``topk``.
+
+    ``q``: [tokens, heads, dim], bfloat16, float16 or float8_e4m3fn.  ``weights``: float32
+    [tokens, heads].  ``keys``: [pages, page_size, dim] of q's type, ``key_scale`` float32
+    [pages, page_size] or None.  ``block_table``: int32 [sequences, width], the pages of each
+    sequence in order.  ``end``: int32 [tokens], the keys each query sees (the ``end`` of
+    ``topk``).  ``seq_ids``: int32 [tokens], each query's sequence; None: query t is of
+    sequence t, or all are of the only one.
+
+    Returns [tokens, row_stride] in ``out_dtype`` (bfloat16, or float32), -inf where a query
+    sees no key; ``row_stride`` defaults to the keys a table row can name, rounded up to the
+    TopK row-stride requirement.  ``out`` may supply that tensor.
+    """
+    import torch
+
+    dt = _operand_dtype("q", q, True)
+    dev, tokens, t_stride = _queries(q, block_table, end, seq_ids)
+    heads, dim = q.shape[1], q.shape[2]
+    if keys.dtype != q.dtype or keys.device != dev or keys.dim() != 3 or keys.shape[2] != dim or keys.stride(2) != 1:
+        raise ValueError("keys must be [pages, page_size, dim] of q's type on its device, contiguous in the last dimension")
+    if weights.dtype != torch.float32 or weights.shape[1:] != (heads,):
+        raise ValueError("weights must be float32 [tokens, heads]")
+    w_stride = _rows_of("weights", weights, dev, tokens)
+    pages, page = keys.shape[0], keys.shape[1]
+    s_stride = 0
+    if key_scale is not None:
+        if key_scale.dtype != torch.float32 or key_scale.shape != (pages, page):
+            raise ValueError("key_scale must be float32 [pages, page_size]")
+        s_stride = _rows_of("key_scale", key_scale, dev, pages)
+    if out is not None:
+        if out.dim() != 2 or out.device != dev or out.shape[0] != tokens or not out.is_contiguous():
+            raise ValueError("out must be a contiguous tensor [tokens, row_stride]")
+        if (row_stride is not None and out.shape[1] != row_stride) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError("out must have the row_stride and out_dtype that are given")
+        row_stride, out_dtype = out.shape[1], out.dtype
+    else:
+        if row_stride is None:
+            row_stride = (block_table.shape[1] * page + 15) // 16 * 16
+        if out_dtype is None:
+            out_dtype = torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("scores are bfloat16 or float32")
+
+    def call(handle):
+        o = out if out is not None else torch.empty((tokens, row_stride), dtype=out_dtype, device=dev)
+        _check(lib.dsel_index_score(q.data_ptr(), dt, tokens, heads, dim, q.stride(0), q.stride(1), weights.data_ptr(),
+                                    w_stride, keys.data_ptr(), pages, page, keys.stride(0), keys.stride(1),
+                                    _ptr(key_scale), s_stride, block_table.data_ptr(), block_table.shape[0],
+                                    block_table.shape[1], t_stride, _ptr(seq_ids), end.data_ptr(), o.data_ptr(),
+                                    DSEL_F32 if out_dtype == torch.float32 else DSEL_BF16, row_stride, handle))
         return o
 
     return _run(dev, stream, call)

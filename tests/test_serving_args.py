@@ -54,3 +54,48 @@ def test_logits_refusals(kw, err):
 
 def test_logits_zero_rows_is_a_noop():
     assert logits(rows=0, x=None, out=None) == T.DSEL_OK
+
+
+def score(**kw):
+    a = dict(q=0x1000, dtype=T.DSEL_BF16, tokens=4, heads=8, dim=64, q_token_stride=512, q_head_stride=64,
+             weights=0x2000, weights_stride=8, keys=0x3000, pages=10, page_size=16, page_stride=1024, key_stride=64,
+             key_scale=None, scale_page_stride=0, table=0x4000, seqs=4, table_width=5, table_stride=5, seq_ids=None,
+             end=0x5000, out=0x6000, out_dtype=T.DSEL_BF16, row_stride=80, stream=None)
+    a.update(kw)
+    return T.lib.dsel_index_score(*a.values())
+
+
+@pytest.mark.parametrize("kw,err", [
+    (dict(dtype=T.DSEL_F32), "DSEL_ERR_DTYPE"),
+    (dict(dtype=4), "DSEL_ERR_DTYPE"),
+    (dict(out_dtype=T.DSEL_F16), "DSEL_ERR_DTYPE"),
+    (dict(tokens=-1), "DSEL_ERR_ROWS"),
+    (dict(heads=0), "DSEL_ERR_SHAPE"),
+    (dict(heads=129, weights_stride=129), "DSEL_ERR_SHAPE"),
+    (dict(dim=48), "DSEL_ERR_SHAPE"),
+    (dict(dim=160), "DSEL_ERR_SHAPE"),
+    (dict(page_size=0), "DSEL_ERR_SHAPE"),
+    (dict(pages=-1), "DSEL_ERR_SHAPE"),
+    (dict(seqs=3), "DSEL_ERR_SHAPE"),            # neither one sequence nor one for each query
+    (dict(row_stride=72), "DSEL_ERR_STRIDE"),
+    (dict(row_stride=0), "DSEL_ERR_STRIDE"),
+    (dict(q_head_stride=32), "DSEL_ERR_STRIDE"),
+    (dict(q_head_stride=68), "DSEL_ERR_STRIDE"),     # not 16 bytes
+    (dict(q_token_stride=516), "DSEL_ERR_STRIDE"),
+    (dict(key_stride=68), "DSEL_ERR_STRIDE"),
+    (dict(page_stride=1028), "DSEL_ERR_STRIDE"),
+    (dict(weights_stride=7), "DSEL_ERR_STRIDE"),
+    (dict(table_stride=4), "DSEL_ERR_STRIDE"),
+    (dict(q=None), "DSEL_ERR_NULL"),
+    (dict(weights=None), "DSEL_ERR_NULL"),
+    (dict(end=None), "DSEL_ERR_NULL"),
+    (dict(q=0x1008), "DSEL_ERR_ALIGN"),
+    (dict(keys=0x3008), "DSEL_ERR_ALIGN"),
+    (dict(out=0x6008), "DSEL_ERR_ALIGN"),
+])
+def test_score_refusals(kw, err):
+    assert score(**kw) == header_define(err)
+
+
+def test_score_zero_tokens_is_a_noop():
+    assert score(tokens=0, q=None, out=None, seqs=0) == T.DSEL_OK
