@@ -395,6 +395,46 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
                               int64_t table_stride, const int32_t* seq_ids, const int32_t* end, void* out,
                               int out_dtype, int64_t row_stride, void* stream);
 
+/*
+ * dsel_sparse_attn -- attention of each query over the cached blocks that its TopK
+ * indices name.
+ *   z[n] = scale * sum_d q[t][h][d] * k[n][d];  o[t][h] = softmax(z) v;
+ *   lse[t][h] = log sum_n exp(z[n])
+ * where n runs over the positions i * block .. i * block + block - 1 of every index
+ * i of query t's list that lie before end[t] and exist (above).  Indices below 0
+ * (dsel_topk's sentinels) are skipped; an index that is listed twice counts twice.
+ * Query head h reads key head h / (q_heads / kv_heads).  Products and sums in
+ * float32, the probabilities rounded to `dtype` for the product with v, o rounded
+ * once.  A query with nothing to read, or only scores of -inf, gets o = 0 and
+ * lse = -inf; what lies in keys and values that it does not read has no effect.
+ *   q            device [tokens][q_heads][dim] of `dtype` (DSEL_BF16 / _F16), strides in
+ *                elements; dim 64 or 128; q_heads a multiple of kv_heads
+ *   k, v         device [pages][page_size][kv_heads][dim] of `dtype`, strides in elements
+ *                (page_size any).  Bases 16-byte aligned, strides multiples of 8.
+ *   table, seqs, table_width, table_stride, seq_ids, end
+ *                as for dsel_index_score (end[t] counts positions, not blocks)
+ *   indices      device int32 or int64 (index_dtype) [tokens][take], or one list for each
+ *                key head: entry j of query t and key head g at
+ *                t * idx_token_stride + g * idx_head_stride + j (idx_head_stride 0: shared)
+ *   block        positions an index stands for (1: it is a position itself);
+ *                take * block < 2^30
+ *   out          device [tokens][q_heads][dim] of `dtype`, contiguous, 16-byte aligned
+ *   lse          device float32 [tokens][q_heads], or NULL
+ * The outputs may share no memory with the inputs.  The result does not depend on
+ * scheduling (no atomics).
+ * Returns DSEL_OK, DSEL_ERR_DTYPE / _INDEX_DTYPE / _ROWS / _SHAPE / _STRIDE / _NULL /
+ * _ALIGN / _DEVICE or DSEL_ERR_CUDA.  One launch, asynchronous on `stream`, no
+ * workspace; can be captured.
+ */
+DSEL_API int dsel_sparse_attn(const void* q, int dtype, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                              int64_t q_token_stride, int64_t q_head_stride, const void* k, const void* v,
+                              int32_t pages, int32_t page_size, int64_t k_page_stride, int64_t k_row_stride,
+                              int64_t k_head_stride, int64_t v_page_stride, int64_t v_row_stride,
+                              int64_t v_head_stride, const int32_t* table, int32_t seqs, int32_t table_width,
+                              int64_t table_stride, const int32_t* seq_ids, const int32_t* end, const void* indices,
+                              int index_dtype, int32_t take, int64_t idx_token_stride, int64_t idx_head_stride,
+                              int32_t block, float scale, void* out, float* lse, void* stream);
+
 /* Row-stride requirement in elements for `dtype` (the pages' get_stride_requirement,
  * narracomm paragraph on install and switches): 16 for both dtypes, so every row
  * start is 32-byte (bf16) or 64-byte (f32) aligned.  Returns -1 for a bad dtype. */

@@ -102,3 +102,48 @@ def oracle_score(q, weights, keys, table, end, row_stride, *, seq_ids=None, key_
             err[t, pos] = ((np.abs(w) * a).sum(0) * (dim + 8) * 2.0 ** -23
                            + (np.abs(w) * z).sum(0) * (heads + 8) * 2.0 ** -24) * np.abs(s) + 2.0 ** -120
     return out, err
+
+
+def oracle_attention(q, k_cache, v_cache, table, indices, end, *, block=1, seq_ids=None, scale=None, eps=2.0 ** -8):
+    """(o, lse, bound on o, bound on lse) in float64; ``eps``: half a step of the operands' type.
+
+    A score's sum of dim exact products in float32 is off by at most (dim + 8) * 2^-23 of the sum of
+    magnitudes, its scaling and the subtraction of the maximum by 2^-23 of their magnitudes; powers
+    of two by 2^-21.  A probability then is off by that much absolutely in the exponent (d), plus eps
+    where it is rounded for the product with v (not in the sum), so
+    |o - o'| <= sum_n p_n |v_n| (2 d + eps + (n + 64) * 2^-22), and one rounding of o to its type;
+    lse is off by d and by the rounding of itself."""
+    tokens, hq, dim = q.shape
+    pages, page_size, hk, _ = k_cache.shape
+    scale = dim ** -0.5 if scale is None else scale
+    o = np.zeros((tokens, hq, dim))
+    lse = np.full((tokens, hq), -np.inf)
+    oerr, lerr = np.zeros_like(o), np.zeros_like(lse)
+    with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
+        for t in range(tokens):
+            for g in range(hk):
+                mine = indices[t, g] if indices.ndim == 3 else indices[t]
+                mine = mine[mine >= 0].astype(np.int64)
+                pos = (mine[:, None] * block + np.arange(block)).reshape(-1)
+                pos = pos[pos < int(end[t])]
+                page, place = _slots(table, _sequence(t, seq_ids, table), page_size, pages, pos)
+                page, place = page[page >= 0], place[page >= 0]
+                if len(page) == 0:
+                    continue
+                k, v = k_cache[page, place, g].astype(np.float64), v_cache[page, place, g].astype(np.float64)
+                for h in range(g * (hq // hk), (g + 1) * (hq // hk)):
+                    z = scale * (k @ q[t, h].astype(np.float64))
+                    top = np.max(z)
+                    if top == -np.inf:
+                        continue
+                    e = np.exp(z - top)
+                    p = e / e.sum()
+                    o[t, h] = p @ v
+                    lse[t, h] = top + np.log(e.sum())
+                    a = abs(scale) * (np.abs(k) @ np.abs(q[t, h].astype(np.float64)))
+                    d = np.max(a * (dim + 8) * 2.0 ** -23 + (np.abs(z) + abs(top)) * 2.0 ** -22)
+                    mag = p @ np.abs(v)
+                    oerr[t, h] = mag * (2 * d + eps + (len(page) + 64) * 2.0 ** -22)
+                    oerr[t, h] += (np.abs(o[t, h]) + oerr[t, h]) * eps + 2.0 ** -24 * (eps < 2.0 ** -9)
+                    lerr[t, h] = d + (len(page) + 64) * 2.0 ** -22 + abs(lse[t, h]) * 2.0 ** -22
+    return o, lse, oerr, lerr

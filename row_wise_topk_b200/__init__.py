@@ -84,6 +84,10 @@ def _load() -> ctypes.CDLL:
     lib.dsel_index_score.restype = c_int
     lib.dsel_index_score.argtypes = [vp, c_int, c_i64, i32, i32, c_i64, c_i64, vp, c_i64, vp, i32, i32, c_i64, c_i64,
                                      vp, c_i64, vp, i32, i32, c_i64, vp, vp, vp, c_int, c_i64, vp]
+    lib.dsel_sparse_attn.restype = c_int
+    lib.dsel_sparse_attn.argtypes = [vp, c_int, c_i64, i32, i32, i32, c_i64, c_i64, vp, vp, i32, i32, c_i64, c_i64,
+                                     c_i64, c_i64, c_i64, c_i64, vp, i32, i32, c_i64, vp, vp, vp, c_int, i32, c_i64,
+                                     c_i64, i32, ctypes.c_float, vp, vp, vp]
     lib.dsel_stride_requirement.restype = c_i64
     lib.dsel_stride_requirement.argtypes = [c_int]
     lib.dsel_status_string.restype = ctypes.c_char_p
@@ -308,4 +312,4 @@ def topk_sample(logits, k: int, u, *, temperature: float = 1.0, top_p: float = 1
 
 
 # the operators before and after the selection (same manner: torch tensors in, one library call)
-from .serving import index_score, process_logits  # noqa: E402,F401
+from .serving import index_score, process_logits, sparse_attention  # noqa: E402,F401

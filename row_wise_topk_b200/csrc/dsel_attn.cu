@@ -1,0 +1,545 @@
+// dsel_sparse_attn: attention of each query over the cached blocks that its TopK
+// indices name.
+//
+//   z[n] = scale * q[t][h] . k[n]   over the listed positions n < end[t]
+//   o[t][h] = sum_n exp(z[n] - m) v[n] / sum_n exp(z[n] - m),   lse = m + log(sum)
+//
+// What bounds it: every query has its own list, so the keys and values are gathered
+// once per (query, key head): 4 * dim bytes for 4 * dim * group operations (group =
+// query heads that share a key head), far below what the tensor cores need.  The work
+// is to keep enough gathers in flight.  So the list of a (query, key head) is dealt out
+// in tiles of 32 positions to the key groups (one or more warps) of a cluster of up to
+// eight CTAs; each group runs its own ring of 16-byte asynchronous copies and its own
+// running maximum and sum, with no barrier but its own; the groups' partial sums meet
+// once, at the end, through distributed shared memory (one launch, no workspace).
+// A group has a warp for every 16 query heads: legacy m16n8k16 products, since a tile
+// has 16 to 64 rows and its operands arrive row by row in any order.
+//
+// Probabilities are rounded to the operands' type for the product with v (the matrix
+// instruction takes both of one type); their sum is kept of the float32 values.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "dsel_ops.cuh"
+
+namespace dsel {
+namespace {
+
+constexpr int kAtWarps = 4;
+constexpr int kAtThreads = kAtWarps * 32;
+constexpr int kAtTile = 32;        // positions per tile
+constexpr int kAtMaxStages = 3;
+constexpr int kAtMaxCluster = 8;
+constexpr int kPitchPad = 8;       // floats: rows of the partial sums fall on different banks
+
+struct AttnParams {
+  const uint8_t* q;
+  int64_t q_token_bytes, q_head_bytes;
+  const uint8_t* k;
+  const uint8_t* v;
+  int64_t k_page_bytes, k_row_bytes, k_head_bytes;
+  int64_t v_page_bytes, v_row_bytes, v_head_bytes;
+  const int32_t* table;
+  int64_t table_stride;
+  const void* indices;
+  int64_t idx_token_stride, idx_head_stride;
+  const int32_t* seq_ids;
+  const int32_t* end;
+  void* out;
+  float* lse;
+  float scale_log2;     // scale * log2(e): the softmax runs on powers of two
+  int32_t idx_i64;
+  int32_t pages, page_size, page_shift;
+  int32_t seqs, table_width, seq_mode;
+  int32_t kv_heads, group, row_tiles;
+  int32_t take, block, block_shift;
+  int32_t tiles;        // tiles of the whole list
+  int32_t stages;
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+template <bool kBf16>
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (kBf16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if (kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float peer_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Warps that share a key group: its own barrier, or none for a single warp.
+template <int kRowWarps>
+__device__ __forceinline__ void group_sync(int group) {
+  if (kRowWarps == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kRowWarps * 32) : "memory");
+}
+
+// Position in its sequence of entry l of the list, or -1: none, or behind `end`.
+__device__ __forceinline__ int32_t list_position(const AttnParams& p, const void* idx, int32_t l, int32_t end) {
+  const int32_t j = p.block_shift >= 0 ? l >> p.block_shift : l / p.block;
+  if (j >= p.take) return -1;
+  const int64_t i = p.idx_i64 ? static_cast<const int64_t*>(idx)[j] : int64_t(static_cast<const int32_t*>(idx)[j]);
+  if (i < 0 || i > int64_t(end)) return -1;
+  const int64_t pos = i * p.block + (l - j * p.block);
+  return pos < int64_t(end) ? int32_t(pos) : -1;
+}
+
+struct Place {
+  int64_t k, v;   // byte offsets of the rows; k < 0: none
+};
+__device__ __forceinline__ Place locate(const AttnParams& p, const int32_t* table, int32_t pos) {
+  Place at = {-1, -1};
+  if (pos >= 0) {
+    const int32_t i = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
+    int32_t page = -1;
+    if (i < p.table_width) page = table[i];
+    if (page >= 0 && page < p.pages) {
+      const int64_t r = pos - i * p.page_size;
+      at.k = int64_t(page) * p.k_page_bytes + r * p.k_row_bytes;
+      at.v = int64_t(page) * p.v_page_bytes + r * p.v_row_bytes;
+    }
+  }
+  return at;
+}
+
+template <bool kBf16, int kDim, int kRowWarps>
+__global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant__ AttnParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kGroups = kAtWarps / kRowWarps;          // key groups of the CTA
+  constexpr int kRows = 16 * kRowWarps;                  // query heads of the CTA
+  constexpr int kRowBytes = kDim * 2;
+  constexpr int kPieces = kRowBytes / 16;
+  constexpr int kTileBytes = kAtTile * kRowBytes;        // keys of a tile; its values follow
+  constexpr int kPitch = kDim + kPitchPad;
+  const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
+  const int grp = warp / kRowWarps, rw = warp % kRowWarps;
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  const int32_t unit = int32_t(blockIdx.x / ranks);
+  const int32_t rt = unit % p.row_tiles;
+  const int32_t th = unit / p.row_tiles;
+  const int32_t kvh = th % p.kv_heads;
+  const int32_t t = th / p.kv_heads;
+  grid_wait();
+  grid_launch();
+
+  int32_t end = p.end[t];
+  const int32_t seq = p.seq_mode == 0 ? p.seq_ids[t] : (p.seq_mode == 1 ? t : 0);
+  if (seq < 0 || seq >= p.seqs) end = 0;
+  const int32_t* table = p.table + (end > 0 ? int64_t(seq) * p.table_stride : 0);
+  const int64_t idx_off = int64_t(t) * p.idx_token_stride + int64_t(kvh) * p.idx_head_stride;
+  const void* idx = static_cast<const uint8_t*>(p.indices) + idx_off * (p.idx_i64 ? 8 : 4);
+  const uint8_t* kbase = p.k + int64_t(kvh) * p.k_head_bytes;
+  const uint8_t* vbase = p.v + int64_t(kvh) * p.v_head_bytes;
+
+  // this warp's query heads as A fragments
+  const int row0 = rt * kRows + rw * 16;    // first head of the group
+  uint32_t qf[kDim / 16][4];
+  {
+    const uint8_t* qb = p.q + int64_t(t) * p.q_token_bytes + (lane & 3) * 4;
+    const int ra = row0 + (lane >> 2), rb = ra + 8;
+    const uint8_t* qa = qb + int64_t(kvh * p.group + ra) * p.q_head_bytes;
+    const uint8_t* qc = qb + int64_t(kvh * p.group + rb) * p.q_head_bytes;
+#pragma unroll
+    for (int s = 0; s < kDim / 16; ++s) {
+      qf[s][0] = ra < p.group ? *reinterpret_cast<const uint32_t*>(qa + s * 32) : 0u;
+      qf[s][1] = rb < p.group ? *reinterpret_cast<const uint32_t*>(qc + s * 32) : 0u;
+      qf[s][2] = ra < p.group ? *reinterpret_cast<const uint32_t*>(qa + s * 32 + 16) : 0u;
+      qf[s][3] = rb < p.group ? *reinterpret_cast<const uint32_t*>(qc + s * 32 + 16) : 0u;
+    }
+  }
+
+  float o[kDim / 8][4];
+#pragma unroll
+  for (int i = 0; i < kDim / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float m0 = -__int_as_float(0x7F800000), m1 = m0, l0 = 0.f, l1 = 0.f;
+
+  const uint32_t ring = shared_addr(smem) + uint32_t(grp * p.stages) * (2 * kTileBytes);
+  const int32_t step = int32_t(ranks) * kGroups;
+  const int32_t first = int32_t(rank) * kGroups + grp;
+  const int32_t mine = p.tiles > first ? (p.tiles - first + step - 1) / step : 0;   // tiles of this group
+
+  // Two loads lie between a list entry and its rows (the index, the page): each is fetched a tile ahead of its use.
+  int32_t pos_next = mine > 0 ? list_position(p, idx, first * kAtTile + lane, end) : -1;
+  auto issue = [&](int32_t i) {   // starts the copies of the group's tile i
+    if (i < mine) {
+      const Place at = locate(p, table, pos_next);
+      pos_next = i + 1 < mine ? list_position(p, idx, (first + (i + 1) * step) * kAtTile + lane, end) : -1;
+      const uint32_t any = __ballot_sync(0xFFFFFFFFu, at.k >= 0);
+      if (any != 0u) {
+        const uint32_t dst = ring + uint32_t(i % p.stages) * (2 * kTileBytes);
+        constexpr int kPerPass = 32 / kPieces;   // rows per pass of a warp
+        const int piece = lane % kPieces;
+#pragma unroll
+        for (int r = 0; r < kAtTile / kRowWarps; r += kPerPass) {
+          const int row = rw * (kAtTile / kRowWarps) + r + lane / kPieces;
+          const int64_t ok = __shfl_sync(0xFFFFFFFFu, at.k, row);
+          const int64_t ov = __shfl_sync(0xFFFFFFFFu, at.v, row);
+          const uint32_t to = dst + uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4);
+          copy16(to, kbase + (ok >= 0 ? ok + piece * 16 : 0), ok >= 0);
+          copy16(to + kTileBytes, vbase + (ok >= 0 ? ov + piece * 16 : 0), ok >= 0);
+        }
+      }
+      return any;
+    }
+    return 0u;
+  };
+
+  uint32_t live[kAtMaxStages];   // which positions of the tiles in flight exist
+#pragma unroll
+  for (int s = 0; s < kAtMaxStages; ++s) live[s] = 0u;
+#pragma unroll
+  for (int s = 0; s < kAtMaxStages - 1; ++s) {
+    if (s < p.stages - 1) live[s] = issue(s);
+    copy_commit();
+  }
+  for (int32_t i = 0; i < mine; ++i) {
+    // (with fewer than kAtMaxStages stages the ring is only that deep: the newest group is this tile's own)
+    const uint32_t newest = issue(i + p.stages - 1);
+    copy_commit();
+    if (p.stages == 3) {
+      live[2] = newest;
+      copy_wait<2>();
+    } else if (p.stages == 2) {
+      live[1] = newest;
+      copy_wait<1>();
+    } else {
+      live[0] = newest;
+      copy_wait<0>();
+    }
+    group_sync<kRowWarps>(grp);
+    const uint32_t here = live[0];
+    live[0] = live[1];
+    live[1] = live[2];
+    if (here != 0u) {
+      const uint32_t kt = ring + uint32_t(i % p.stages) * (2 * kTileBytes);
+      const uint32_t vt = kt + kTileBytes;
+      float s[kAtTile / 8][4];
+#pragma unroll
+      for (int n = 0; n < kAtTile / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+      for (int d = 0; d < kDim / 16; ++d) {
+#pragma unroll
+        for (int n = 0; n < kAtTile / 16; ++n) {   // 16 keys: two column tiles, both halves of the depth
+          const int row = n * 16 + (lane & 7) + ((lane >> 4) << 3);
+          const int piece = d * 2 + ((lane >> 3) & 1);
+          uint32_t b[4];
+          ldmatrix4(kt + uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4), b);
+          mma16816<kBf16>(s[2 * n], qf[d], b[0], b[1]);
+          mma16816<kBf16>(s[2 * n + 1], qf[d], b[2], b[3]);
+        }
+      }
+      // scores as powers of two; positions that do not exist do not count
+      float x0 = m0, x1 = m1;
+      const uint32_t cols = here >> ((lane & 3) * 2);
+#pragma unroll
+      for (int n = 0; n < kAtTile / 8; ++n) {
+        const bool c0 = (cols >> (n * 8)) & 1u, c1 = (cols >> (n * 8 + 1)) & 1u;
+        s[n][0] = c0 ? s[n][0] * p.scale_log2 : -__int_as_float(0x7F800000);
+        s[n][1] = c1 ? s[n][1] * p.scale_log2 : -__int_as_float(0x7F800000);
+        s[n][2] = c0 ? s[n][2] * p.scale_log2 : -__int_as_float(0x7F800000);
+        s[n][3] = c1 ? s[n][3] * p.scale_log2 : -__int_as_float(0x7F800000);
+        x0 = fmaxf(x0, fmaxf(s[n][0], s[n][1]));
+        x1 = fmaxf(x1, fmaxf(s[n][2], s[n][3]));
+      }
+      x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1));
+      x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 2));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 2));
+      if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
+        // (a row without a score so far has m = -inf and holds zeros: any factor is right, but -inf - -inf is not one)
+        const float f0 = x0 == m0 ? 1.f : pow2(m0 - x0), f1 = x1 == m1 ? 1.f : pow2(m1 - x1);
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int n = 0; n < kDim / 8; ++n) {
+          o[n][0] *= f0;
+          o[n][1] *= f0;
+          o[n][2] *= f1;
+          o[n][3] *= f1;
+        }
+        m0 = x0;
+        m1 = x1;
+      }
+      const float z0 = m0 == -__int_as_float(0x7F800000) ? 0.f : m0, z1 = m1 == -__int_as_float(0x7F800000) ? 0.f : m1;
+#pragma unroll
+      for (int n = 0; n < kAtTile / 8; ++n) {
+        s[n][0] = pow2(s[n][0] - z0);
+        s[n][1] = pow2(s[n][1] - z0);
+        s[n][2] = pow2(s[n][2] - z1);
+        s[n][3] = pow2(s[n][3] - z1);
+        l0 += s[n][0] + s[n][1];
+        l1 += s[n][2] + s[n][3];
+      }
+#pragma unroll
+      for (int n = 0; n < kAtTile / 16; ++n) {
+        const uint32_t a[4] = {pack16<kBf16>(s[2 * n][0], s[2 * n][1]), pack16<kBf16>(s[2 * n][2], s[2 * n][3]),
+                               pack16<kBf16>(s[2 * n + 1][0], s[2 * n + 1][1]),
+                               pack16<kBf16>(s[2 * n + 1][2], s[2 * n + 1][3])};
+#pragma unroll
+        for (int d = 0; d < kDim / 16; ++d) {
+          const int row = n * 16 + (lane & 15);
+          const int piece = d * 2 + (lane >> 4);
+          uint32_t b[4];
+          ldmatrix4t(vt + uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4), b);
+          mma16816<kBf16>(o[2 * d], a, b[0], b[1]);
+          mma16816<kBf16>(o[2 * d + 1], a, b[2], b[3]);
+        }
+      }
+    }
+    group_sync<kRowWarps>(grp);   // the stage may be filled again
+  }
+  copy_wait<0>();
+  l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 1);
+  l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 2);
+  l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 1);
+  l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 2);
+
+  // ---- the groups' partial sums meet ----
+  __syncthreads();   // the rings are no longer read
+  float* part = reinterpret_cast<float*>(smem);                       // [kGroups][kRows][kPitch]
+  float* ml = part + kGroups * kRows * kPitch;                        // [kGroups][kRows][2]: maximum, sum
+  float* wt = ml + kGroups * kRows * 2;                               // [ranks * kGroups][kRows], then [kRows] totals
+  {
+    const int r = rw * 16 + (lane >> 2);
+    float* pa = part + (grp * kRows + r) * kPitch + (lane & 3) * 2;
+#pragma unroll
+    for (int n = 0; n < kDim / 8; ++n) {
+      *reinterpret_cast<float2*>(pa + n * 8) = make_float2(o[n][0], o[n][1]);
+      *reinterpret_cast<float2*>(pa + 8 * kPitch + n * 8) = make_float2(o[n][2], o[n][3]);
+    }
+    if ((lane & 3) == 0) {
+      ml[(grp * kRows + r) * 2] = m0;
+      ml[(grp * kRows + r) * 2 + 1] = l0;
+      ml[(grp * kRows + r + 8) * 2] = m1;
+      ml[(grp * kRows + r + 8) * 2 + 1] = l1;
+    }
+  }
+  if (ranks > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  const int parts = int(ranks) * kGroups;
+  float* total = wt + parts * kRows;
+  if (int(threadIdx.x) < kRows) {
+    const int r = int(threadIdx.x);
+    float top = -__int_as_float(0x7F800000);
+    for (int i = 0; i < parts; ++i) {
+      const float mi = peer_load(peer_addr(shared_addr(ml + ((i % kGroups) * kRows + r) * 2), uint32_t(i / kGroups)));
+      wt[i * kRows + r] = mi;
+      top = fmaxf(top, mi);
+    }
+    const float z = top == -__int_as_float(0x7F800000) ? 0.f : top;
+    float sum = 0.f;
+    for (int i = 0; i < parts; ++i) {
+      const float li = peer_load(peer_addr(shared_addr(ml + ((i % kGroups) * kRows + r) * 2 + 1), uint32_t(i / kGroups)));
+      const float w = pow2(wt[i * kRows + r] - z);
+      wt[i * kRows + r] = w;
+      sum += li * w;
+    }
+    total[r] = sum;
+    const int head = rt * kRows + r;
+    if (rank == 0 && p.lse != nullptr && head < p.group)
+      p.lse[int64_t(t) * p.kv_heads * p.group + kvh * p.group + head] =
+          sum == 0.f ? -__int_as_float(0x7F800000) : (z + log2f(sum)) * 0.6931471805599453f;
+  }
+  __syncthreads();
+  for (int i = int(rank) * kAtThreads + int(threadIdx.x); i < kRows * kDim / 4; i += int(ranks) * kAtThreads) {
+    const int r = i / (kDim / 4), c = (i % (kDim / 4)) * 4;
+    const int head = rt * kRows + r;
+    if (head >= p.group) continue;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < parts; ++j) {
+      const float w = wt[j * kRows + r];
+      const float4 b = peer_load4(peer_addr(shared_addr(part + ((j % kGroups) * kRows + r) * kPitch + c), uint32_t(j / kGroups)));
+      a.x += b.x * w;
+      a.y += b.y * w;
+      a.z += b.z * w;
+      a.w += b.w * w;
+    }
+    const float sum = total[r];
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const uint2 y = make_uint2(pack16<kBf16>(a.x * inv, a.y * inv), pack16<kBf16>(a.z * inv, a.w * inv));
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) +
+                              ((int64_t(t) * p.kv_heads * p.group + kvh * p.group + head) * kDim + c) * 2) = y;
+  }
+  if (ranks > 1) cluster_sync_all();   // no CTA leaves while a peer may still read its sums
+}
+
+template <bool kBf16, int kDim, int kRowWarps>
+int launch_attn(AttnParams p, int64_t units, int sms, cudaStream_t st) {
+  auto kern = attn_kernel<kBf16, kDim, kRowWarps>;
+  constexpr int kGroups = kAtWarps / kRowWarps;
+  constexpr int kStageBytes = kGroups * 2 * kAtTile * kDim * 2;
+  // CTAs per (query, key head): as many as fill the SMs twice, but none without a tile for each of its groups
+  int cluster = 1;
+  while (cluster < kAtMaxCluster && units * cluster * 2 <= int64_t(sms) * 2 && cluster * 2 * kGroups <= p.tiles) cluster *= 2;
+  const int64_t each = (p.tiles + int64_t(cluster) * kGroups - 1) / (int64_t(cluster) * kGroups);
+  p.stages = each < 1 ? 1 : (each > kAtMaxStages ? kAtMaxStages : int(each));
+  const int merge = kAtWarps * 16 * (kDim + kPitchPad + 2) * 4 + (cluster * kGroups + 1) * 16 * kRowWarps * 4;
+  const int smem = p.stages * kStageBytes > merge ? p.stages * kStageBytes : merge;
+  if (units * cluster > INT32_MAX) return DSEL_ERR_ROWS;
+  if (allow_smem(reinterpret_cast<const void*>(kern), kAtMaxStages * kStageBytes > 64 * 1024 ? kAtMaxStages * kStageBytes : 64 * 1024) !=
+      cudaSuccess)
+    return DSEL_ERR_CUDA;
+  return launch_dependent(kern, unsigned(units * cluster), kAtThreads, cluster, uint32_t(smem), st, p) == cudaSuccess
+             ? DSEL_OK
+             : DSEL_ERR_CUDA;
+}
+
+template <bool kBf16, int kDim>
+int launch_rows(AttnParams& p, int64_t tokens, int sms, cudaStream_t st) {
+  // a warp for every 16 heads that share keys, up to 64 rows a CTA
+  const int rows = p.group <= 16 ? 16 : p.group <= 32 ? 32 : 64;
+  p.row_tiles = (p.group + rows - 1) / rows;
+  const int64_t units = tokens * p.kv_heads * p.row_tiles;
+  if (rows == 16) return launch_attn<kBf16, kDim, 1>(p, units, sms, st);
+  if (rows == 32) return launch_attn<kBf16, kDim, 2>(p, units, sms, st);
+  return launch_attn<kBf16, kDim, 4>(p, units, sms, st);
+}
+
+int log2_of(int32_t n) {
+  for (int s = 0; s < 31; ++s)
+    if ((int64_t(1) << s) == n) return s;
+  return -1;
+}
+
+}  // namespace
+}  // namespace dsel
+
+using namespace dsel;
+
+DSEL_API int dsel_sparse_attn(const void* q, int dtype, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                              int64_t q_token_stride, int64_t q_head_stride, const void* k, const void* v,
+                              int32_t pages, int32_t page_size, int64_t k_page_stride, int64_t k_row_stride,
+                              int64_t k_head_stride, int64_t v_page_stride, int64_t v_row_stride,
+                              int64_t v_head_stride, const int32_t* table, int32_t seqs, int32_t table_width,
+                              int64_t table_stride, const int32_t* seq_ids, const int32_t* end, const void* indices,
+                              int index_dtype, int32_t take, int64_t idx_token_stride, int64_t idx_head_stride,
+                              int32_t block, float scale, void* out, float* lse, void* stream) {
+  if (dtype != DSEL_BF16 && dtype != DSEL_F16) return DSEL_ERR_DTYPE;
+  if (index_dtype != DSEL_I32 && index_dtype != DSEL_I64) return DSEL_ERR_INDEX_DTYPE;
+  if (tokens < 0 || tokens > INT32_MAX / 2) return DSEL_ERR_ROWS;
+  if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0 || (dim != 64 && dim != 128)) return DSEL_ERR_SHAPE;
+  if (pages < 0 || page_size < 1 || seqs < 0 || table_width < 0) return DSEL_ERR_SHAPE;
+  if (seq_ids == nullptr && seqs != 1 && int64_t(seqs) != tokens) return DSEL_ERR_SHAPE;
+  if (take < 0 || block < 1 || int64_t(take) * block > INT32_MAX / 2) return DSEL_ERR_SHAPE;
+  if (q_head_stride < dim || q_token_stride < 0 || k_page_stride < 0 || v_page_stride < 0 || k_row_stride < dim ||
+      v_row_stride < dim || k_head_stride < 0 || v_head_stride < 0 || table_stride < table_width ||
+      idx_token_stride < 0 || idx_head_stride < 0)
+    return DSEL_ERR_STRIDE;
+  if (((q_token_stride | q_head_stride | k_page_stride | k_row_stride | k_head_stride | v_page_stride | v_row_stride |
+        v_head_stride) & 7) != 0)
+    return DSEL_ERR_STRIDE;   // rows are copied in 16-byte pieces
+  if (tokens == 0) return DSEL_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || table == nullptr || end == nullptr || out == nullptr ||
+      (indices == nullptr && take > 0))
+    return DSEL_ERR_NULL;
+  if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+        reinterpret_cast<uintptr_t>(out)) & 15u) != 0)
+    return DSEL_ERR_ALIGN;
+  if (const int st = check_device(); st != DSEL_OK) return st;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return DSEL_ERR_CUDA;
+  AttnParams p = {};
+  p.q = static_cast<const uint8_t*>(q);
+  p.q_token_bytes = q_token_stride * 2;
+  p.q_head_bytes = q_head_stride * 2;
+  p.k = static_cast<const uint8_t*>(k);
+  p.v = static_cast<const uint8_t*>(v);
+  p.k_page_bytes = k_page_stride * 2;
+  p.k_row_bytes = k_row_stride * 2;
+  p.k_head_bytes = k_head_stride * 2;
+  p.v_page_bytes = v_page_stride * 2;
+  p.v_row_bytes = v_row_stride * 2;
+  p.v_head_bytes = v_head_stride * 2;
+  p.table = table;
+  p.table_stride = table_stride;
+  p.indices = indices;
+  p.idx_token_stride = idx_token_stride;
+  p.idx_head_stride = idx_head_stride;
+  p.idx_i64 = index_dtype == DSEL_I64;
+  p.seq_ids = seq_ids;
+  p.end = end;
+  p.out = out;
+  p.lse = lse;
+  p.scale_log2 = float(double(scale) * 1.4426950408889634);
+  p.pages = pages;
+  p.page_size = page_size;
+  p.page_shift = log2_of(page_size);
+  p.seqs = seqs;
+  p.table_width = table_width;
+  p.seq_mode = seq_ids != nullptr ? 0 : (seqs == 1 ? 2 : 1);
+  p.kv_heads = kv_heads;
+  p.group = q_heads / kv_heads;
+  p.take = take;
+  p.block = block;
+  p.block_shift = log2_of(block);
+  p.tiles = int32_t((int64_t(take) * block + kAtTile - 1) / kAtTile);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (dtype == DSEL_BF16)
+    return dim == 64 ? launch_rows<true, 64>(p, tokens, sms, cs) : launch_rows<true, 128>(p, tokens, sms, cs);
+  return dim == 64 ? launch_rows<false, 64>(p, tokens, sms, cs) : launch_rows<false, 128>(p, tokens, sms, cs);
+}

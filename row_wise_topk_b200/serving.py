@@ -4,6 +4,7 @@
   for repeated tokens, biases, a grammar mask.
 - ``index_score`` makes the rows that ``topk`` selects keys from: the Lightning Indexer's
   score of every cached key for each query.
+- ``sparse_attention`` reads the blocks that those indices name out of a paged cache.
 
 Each is one call of the C ABI (``include/dsel.h`` states the formulas and the argument
 rules); this module checks the tensors and allocates the outputs.  Calls run on the
@@ -244,5 +245,61 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
                                     block_table.shape[1], t_stride, _ptr(seq_ids), end.data_ptr(), o.data_ptr(),
                                     DSEL_F32 if out_dtype == torch.float32 else DSEL_BF16, row_stride, handle))
         return o
+
+    return _run(dev, stream, call)
+
+
+def sparse_attention(q, k_cache, v_cache, block_table, indices, end, *, block=1, seq_ids=None, scale=None, out=None,
+                     return_lse=False, stream=None):
+    """Attention of each query over the cached blocks its indices name (``dsel_sparse_attn``).
+
+    ``q``: [tokens, q_heads, dim], bfloat16 or float16, dim 64 or 128.  ``k_cache`` / ``v_cache``:
+    [pages, page_size, kv_heads, dim] of q's type; query head h reads key head
+    h // (q_heads // kv_heads).  ``block_table``, ``end`` (positions each query sees) and
+    ``seq_ids``: as for ``index_score``.  ``indices``: int32 or int64 [tokens, k], or
+    [tokens, kv_heads, k] for a list per key head: what ``topk`` returns; an index i stands for
+    the positions i * block .. i * block + block - 1, negative ones are skipped.  ``scale``
+    defaults to dim ** -0.5.
+
+    Returns [tokens, q_heads, dim] (``out`` may supply it), and with ``return_lse`` also the
+    float32 logarithms of the sums of exponentials [tokens, q_heads].
+    """
+    import torch
+
+    dt = _operand_dtype("q", q, False)
+    dev, tokens, t_stride = _queries(q, block_table, end, seq_ids)
+    heads, dim = q.shape[1], q.shape[2]
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if c.dtype != q.dtype or c.device != dev or c.dim() != 4 or c.shape[3] != dim or c.stride(3) != 1:
+            raise ValueError(f"{name} must be [pages, page_size, kv_heads, dim] of q's type on its device, "
+                             "contiguous in the last dimension")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    pages, page, kv_heads = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
+    i_dt = _index_dtype("indices", indices)
+    if indices.device != dev or indices.dim() not in (2, 3) or indices.shape[0] != tokens:
+        raise ValueError("indices must be [tokens, k] or [tokens, kv_heads, k] on q's device")
+    if indices.dim() == 3 and indices.shape[1] != kv_heads:
+        raise ValueError("indices must have one list, or one for each key head")
+    take = indices.shape[-1]
+    if take > 1 and indices.stride(-1) != 1:
+        raise ValueError("indices must be contiguous in the last dimension")
+    if scale is None:
+        scale = dim ** -0.5
+    if out is not None and (out.dtype != q.dtype or out.device != dev or out.shape != (tokens, heads, dim)
+                            or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous tensor of q's shape and type")
+
+    def call(handle):
+        o = out if out is not None else torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
+        _check(lib.dsel_sparse_attn(q.data_ptr(), dt, tokens, heads, kv_heads, dim, q.stride(0), q.stride(1),
+                                    k_cache.data_ptr(), v_cache.data_ptr(), pages, page, *k_cache.stride()[:3],
+                                    *v_cache.stride()[:3], block_table.data_ptr(), block_table.shape[0],
+                                    block_table.shape[1], t_stride, _ptr(seq_ids), end.data_ptr(),
+                                    indices.data_ptr(), i_dt, take, indices.stride(0),
+                                    indices.stride(1) if indices.dim() == 3 else 0, block, scale, o.data_ptr(),
+                                    _ptr(lse), handle))
+        return (o, lse) if return_lse else o
 
     return _run(dev, stream, call)

@@ -99,3 +99,47 @@ def test_score_refusals(kw, err):
 
 def test_score_zero_tokens_is_a_noop():
     assert score(tokens=0, q=None, out=None, seqs=0) == T.DSEL_OK
+
+
+def attn(**kw):
+    a = dict(q=0x1000, dtype=T.DSEL_BF16, tokens=4, q_heads=8, kv_heads=2, dim=64, q_token_stride=512,
+             q_head_stride=64, k=0x2000, v=0x3000, pages=10, page_size=16, k_page_stride=2048, k_row_stride=128,
+             k_head_stride=64, v_page_stride=2048, v_row_stride=128, v_head_stride=64, table=0x4000, seqs=4,
+             table_width=5, table_stride=5, seq_ids=None, end=0x5000, indices=0x6000, index_dtype=T.DSEL_I32, take=7,
+             idx_token_stride=7, idx_head_stride=0, block=16, scale=0.125, out=0x7000, lse=None, stream=None)
+    a.update(kw)
+    return T.lib.dsel_sparse_attn(*a.values())
+
+
+@pytest.mark.parametrize("kw,err", [
+    (dict(dtype=T.DSEL_F32), "DSEL_ERR_DTYPE"),
+    (dict(dtype=T.DSEL_E4M3), "DSEL_ERR_DTYPE"),
+    (dict(index_dtype=2), "DSEL_ERR_INDEX_DTYPE"),
+    (dict(tokens=-1), "DSEL_ERR_ROWS"),
+    (dict(kv_heads=0), "DSEL_ERR_SHAPE"),
+    (dict(kv_heads=3), "DSEL_ERR_SHAPE"),
+    (dict(dim=96), "DSEL_ERR_SHAPE"),
+    (dict(page_size=0), "DSEL_ERR_SHAPE"),
+    (dict(seqs=3), "DSEL_ERR_SHAPE"),
+    (dict(take=-1), "DSEL_ERR_SHAPE"),
+    (dict(block=0), "DSEL_ERR_SHAPE"),
+    (dict(take=1 << 20, block=1 << 12), "DSEL_ERR_SHAPE"),
+    (dict(q_head_stride=60), "DSEL_ERR_STRIDE"),
+    (dict(q_token_stride=516), "DSEL_ERR_STRIDE"),
+    (dict(k_row_stride=56), "DSEL_ERR_STRIDE"),
+    (dict(k_page_stride=2052), "DSEL_ERR_STRIDE"),
+    (dict(v_head_stride=68), "DSEL_ERR_STRIDE"),
+    (dict(table_stride=4), "DSEL_ERR_STRIDE"),
+    (dict(idx_token_stride=-1), "DSEL_ERR_STRIDE"),
+    (dict(q=None), "DSEL_ERR_NULL"),
+    (dict(indices=None), "DSEL_ERR_NULL"),
+    (dict(out=None), "DSEL_ERR_NULL"),
+    (dict(v=0x3008), "DSEL_ERR_ALIGN"),
+    (dict(out=0x7008), "DSEL_ERR_ALIGN"),
+])
+def test_attn_refusals(kw, err):
+    assert attn(**kw) == header_define(err)
+
+
+def test_attn_zero_tokens_is_a_noop():
+    assert attn(tokens=0, q=None, out=None, seqs=0) == T.DSEL_OK
