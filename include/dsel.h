@@ -435,6 +435,19 @@ DSEL_API int dsel_sparse_attn(const void* q, int dtype, int64_t tokens, int32_t 
                               int index_dtype, int32_t take, int64_t idx_token_stride, int64_t idx_head_stride,
                               int32_t block, float scale, void* out, float* lse, void* stream);
 
+/*
+ * dsel_call -- one of the three calls above with its arguments in an array of 8-byte
+ * words, for bindings that pay for every argument they pass: word i holds argument i
+ * of dsel_logits, dsel_index_score or dsel_sparse_attn (`call`), pointers and integers
+ * as int64_t, `scale` as a double.  Returns what that call returns; DSEL_ERR_NULL for
+ * a NULL array, DSEL_ERR_UNAVAILABLE for another `call`, DSEL_ERR_SHAPE for an integer
+ * that its argument cannot hold.
+ */
+#define DSEL_CALL_LOGITS 0
+#define DSEL_CALL_INDEX_SCORE 1
+#define DSEL_CALL_SPARSE_ATTN 2
+DSEL_API int dsel_call(int call, const void* words);
+
 /* Row-stride requirement in elements for `dtype` (the pages' get_stride_requirement,
  * narracomm paragraph on install and switches): 16 for both dtypes, so every row
  * start is 32-byte (bf16) or 64-byte (f32) aligned.  Returns -1 for a bad dtype. */

@@ -29,6 +29,7 @@ DSEL_KERNEL_STREAM, DSEL_KERNEL_RESIDENT, DSEL_KERNEL_SLICE = 0, 1, 2
 DSEL_OK = 0
 DSEL_ERR_SCRATCH_LIMIT = -16
 DSEL_ERR_SHAPE, DSEL_ERR_OVERLAP = -17, -18
+DSEL_CALL_LOGITS, DSEL_CALL_INDEX_SCORE, DSEL_CALL_SPARSE_ATTN = 0, 1, 2
 DSEL_NOALLOC_SCRATCH_BYTES = 512 * 1024
 
 
@@ -88,6 +89,8 @@ def _load() -> ctypes.CDLL:
     lib.dsel_sparse_attn.argtypes = [vp, c_int, c_i64, i32, i32, i32, c_i64, c_i64, vp, vp, i32, i32, c_i64, c_i64,
                                      c_i64, c_i64, c_i64, c_i64, vp, i32, i32, c_i64, vp, vp, vp, c_int, i32, c_i64,
                                      c_i64, i32, ctypes.c_float, vp, vp, vp]
+    lib.dsel_call.restype = c_int
+    lib.dsel_call.argtypes = [c_int, ctypes.c_char_p]
     lib.dsel_stride_requirement.restype = c_i64
     lib.dsel_stride_requirement.argtypes = [c_int]
     lib.dsel_status_string.restype = ctypes.c_char_p

@@ -428,7 +428,8 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
 }
 
 template <bool kBf16, int kDim, int kRowWarps>
-int launch_attn(AttnParams p, int64_t units, int sms, cudaStream_t st) {
+int launch_attn(AttnParams p, int64_t units, int dev, int sms, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed;
   auto kern = attn_kernel<kBf16, kDim, kRowWarps>;
   constexpr int kGroups = kAtWarps / kRowWarps;
   constexpr int kStageBytes = kGroups * 2 * kAtTile * kDim * 2;
@@ -440,8 +441,8 @@ int launch_attn(AttnParams p, int64_t units, int sms, cudaStream_t st) {
   const int merge = kAtWarps * 16 * (kDim + kPitchPad + 2) * 4 + (cluster * kGroups + 1) * 16 * kRowWarps * 4;
   const int smem = p.stages * kStageBytes > merge ? p.stages * kStageBytes : merge;
   if (units * cluster > INT32_MAX) return DSEL_ERR_ROWS;
-  if (allow_smem(reinterpret_cast<const void*>(kern), kAtMaxStages * kStageBytes > 64 * 1024 ? kAtMaxStages * kStageBytes : 64 * 1024) !=
-      cudaSuccess)
+  if (allow_smem(reinterpret_cast<const void*>(kern), kAtMaxStages * kStageBytes > 64 * 1024 ? kAtMaxStages * kStageBytes : 64 * 1024,
+                 dev, &allowed) != cudaSuccess)
     return DSEL_ERR_CUDA;
   return launch_dependent(kern, unsigned(units * cluster), kAtThreads, cluster, uint32_t(smem), st, p) == cudaSuccess
              ? DSEL_OK
@@ -449,14 +450,14 @@ int launch_attn(AttnParams p, int64_t units, int sms, cudaStream_t st) {
 }
 
 template <bool kBf16, int kDim>
-int launch_rows(AttnParams& p, int64_t tokens, int sms, cudaStream_t st) {
+int launch_rows(AttnParams& p, int64_t tokens, int dev, int sms, cudaStream_t st) {
   // a warp for every 16 heads that share keys, up to 64 rows a CTA
   const int rows = p.group <= 16 ? 16 : p.group <= 32 ? 32 : 64;
   p.row_tiles = (p.group + rows - 1) / rows;
   const int64_t units = tokens * p.kv_heads * p.row_tiles;
-  if (rows == 16) return launch_attn<kBf16, kDim, 1>(p, units, sms, st);
-  if (rows == 32) return launch_attn<kBf16, kDim, 2>(p, units, sms, st);
-  return launch_attn<kBf16, kDim, 4>(p, units, sms, st);
+  if (rows == 16) return launch_attn<kBf16, kDim, 1>(p, units, dev, sms, st);
+  if (rows == 32) return launch_attn<kBf16, kDim, 2>(p, units, dev, sms, st);
+  return launch_attn<kBf16, kDim, 4>(p, units, dev, sms, st);
 }
 
 int log2_of(int32_t n) {
@@ -499,10 +500,8 @@ DSEL_API int dsel_sparse_attn(const void* q, int dtype, int64_t tokens, int32_t 
   if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
         reinterpret_cast<uintptr_t>(out)) & 15u) != 0)
     return DSEL_ERR_ALIGN;
-  if (const int st = check_device(); st != DSEL_OK) return st;
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return DSEL_ERR_CUDA;
+  if (const int st = current_device(&dev, &sms); st != DSEL_OK) return st;
   AttnParams p = {};
   p.q = static_cast<const uint8_t*>(q);
   p.q_token_bytes = q_token_stride * 2;
@@ -540,6 +539,6 @@ DSEL_API int dsel_sparse_attn(const void* q, int dtype, int64_t tokens, int32_t 
   p.tiles = int32_t((int64_t(take) * block + kAtTile - 1) / kAtTile);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (dtype == DSEL_BF16)
-    return dim == 64 ? launch_rows<true, 64>(p, tokens, sms, cs) : launch_rows<true, 128>(p, tokens, sms, cs);
-  return dim == 64 ? launch_rows<false, 64>(p, tokens, sms, cs) : launch_rows<false, 128>(p, tokens, sms, cs);
+    return dim == 64 ? launch_rows<true, 64>(p, tokens, dev, sms, cs) : launch_rows<true, 128>(p, tokens, dev, sms, cs);
+  return dim == 64 ? launch_rows<false, 64>(p, tokens, dev, sms, cs) : launch_rows<false, 128>(p, tokens, dev, sms, cs);
 }

@@ -219,10 +219,11 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(const __grid_constan
 }
 
 template <typename T, typename tok_t>
-int launch_logits(const LogitsParams& p, int64_t rows, bool aligned, cudaStream_t st) {
+int launch_logits(const LogitsParams& p, int64_t rows, bool aligned, int dev, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed[2];
   const uint32_t smem = kLgSlice * 4 * (p.bias_ids != nullptr ? 2 : 1);
   auto kern = aligned ? logits_kernel<T, tok_t, true> : logits_kernel<T, tok_t, false>;
-  if (allow_smem(reinterpret_cast<const void*>(kern), 2 * kLgSlice * 4) != cudaSuccess) return DSEL_ERR_CUDA;
+  if (allow_smem(reinterpret_cast<const void*>(kern), 2 * kLgSlice * 4, dev, &allowed[aligned]) != cudaSuccess) return DSEL_ERR_CUDA;
   return launch_dependent(kern, unsigned(rows * p.slices), kLgThreads, 1, smem, st, p) == cudaSuccess ? DSEL_OK
                                                                                                       : DSEL_ERR_CUDA;
 }
@@ -268,7 +269,8 @@ DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, 
     return DSEL_ERR_OVERLAP;
   LogitsParams p = {};
   p.slices = slices;
-  if (const int st = check_device(); st != DSEL_OK) return st;
+  int dev = 0, sms = 0;
+  if (const int st = current_device(&dev, &sms); st != DSEL_OK) return st;
   p.x = x;
   p.x_stride = x_stride;
   p.tokens = width > 0 ? tokens : nullptr;
@@ -295,7 +297,7 @@ DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, 
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool wide = token_dtype == DSEL_I64;
   if (dtype == DSEL_BF16)
-    return wide ? launch_logits<__nv_bfloat16, int64_t>(p, rows, aligned, cs)
-                : launch_logits<__nv_bfloat16, int32_t>(p, rows, aligned, cs);
-  return wide ? launch_logits<float, int64_t>(p, rows, aligned, cs) : launch_logits<float, int32_t>(p, rows, aligned, cs);
+    return wide ? launch_logits<__nv_bfloat16, int64_t>(p, rows, aligned, dev, cs)
+                : launch_logits<__nv_bfloat16, int32_t>(p, rows, aligned, dev, cs);
+  return wide ? launch_logits<float, int64_t>(p, rows, aligned, dev, cs) : launch_logits<float, int32_t>(p, rows, aligned, dev, cs);
 }

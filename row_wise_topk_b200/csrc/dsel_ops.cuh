@@ -2,6 +2,7 @@
 // sparse attention): launch helpers and thin PTX wrappers.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -12,26 +13,35 @@ namespace dsel {
 
 // ---- host ----
 
-// The current device is an sm_100 GPU (asked once per device).
-inline int check_device() {
-  static int known[64];   // 0 unknown, 1 sm_100; written with the same value by every thread
+// The current device, an sm_100 GPU, and its SM count (asked of the runtime once per device).
+inline int current_device(int* device, int* sms) {
+  static std::atomic<int> known[64];   // SM count, 0: not asked yet; every thread stores the same value
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSEL_ERR_CUDA;
   if (dev < 0 || dev >= 64) return DSEL_ERR_DEVICE;
-  if (known[dev] == 1) return DSEL_OK;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return DSEL_ERR_CUDA;
-  if (major != 10 || minor != 0) return DSEL_ERR_DEVICE;
-  known[dev] = 1;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return DSEL_ERR_CUDA;
+    if (major != 10 || minor != 0) return DSEL_ERR_DEVICE;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  *device = dev;
+  *sms = n;
   return DSEL_OK;
 }
 
-// Lets `kern` use `bytes` of dynamic shared memory on the current device.
-inline cudaError_t allow_smem(const void* kern, int bytes) {
-  return bytes <= 48 * 1024 ? cudaSuccess
-                            : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+// Lets a kernel use `bytes` of dynamic shared memory on device `dev`; `done` is the kernel's
+// own flag word (one bit per device), so that the runtime is asked once.
+inline cudaError_t allow_smem(const void* kern, int bytes, int dev, std::atomic<uint64_t>* done) {
+  const uint64_t bit = uint64_t(1) << dev;
+  if ((done->load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // A launch in clusters of `cluster` CTAs that may begin while the launch before it

@@ -529,9 +529,10 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
 }
 
 template <bool kByte, int kHeads, int kCols>
-int launch_score(const ScoreParams& p, int dtype, int grid, int smem, cudaStream_t st) {
+int launch_score(const ScoreParams& p, int dtype, int grid, int smem, int dev, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed;
   auto kern = score_kernel<kByte, kHeads, kCols>;
-  if (allow_smem(reinterpret_cast<const void*>(kern), kScoreSmem) != cudaSuccess) return DSEL_ERR_CUDA;
+  if (allow_smem(reinterpret_cast<const void*>(kern), kScoreSmem, dev, &allowed) != cudaSuccess) return DSEL_ERR_CUDA;
   // D f32, A and B of the operands' type (f16 0, bf16 1; e4m3 0), both K-major, N / 8, M / 16
   const uint32_t type = dtype == DSEL_BF16 ? 1u : 0u;
   const uint32_t idesc =
@@ -550,18 +551,18 @@ int launch_score(const ScoreParams& p, int dtype, int grid, int smem, cudaStream
 }
 
 template <bool kByte>
-int launch_heads(const ScoreParams& p, int dtype, int hp, bool wide, int grid, int smem, cudaStream_t st) {
+int launch_heads(const ScoreParams& p, int dtype, int hp, bool wide, int grid, int smem, int dev, cudaStream_t st) {
   if (hp == 16)
-    return wide ? launch_score<kByte, 16, 256>(p, dtype, grid, smem, st)
-                : launch_score<kByte, 16, 16>(p, dtype, grid, smem, st);
+    return wide ? launch_score<kByte, 16, 256>(p, dtype, grid, smem, dev, st)
+                : launch_score<kByte, 16, 16>(p, dtype, grid, smem, dev, st);
   if (hp == 32)
-    return wide ? launch_score<kByte, 32, 256>(p, dtype, grid, smem, st)
-                : launch_score<kByte, 32, 32>(p, dtype, grid, smem, st);
+    return wide ? launch_score<kByte, 32, 256>(p, dtype, grid, smem, dev, st)
+                : launch_score<kByte, 32, 32>(p, dtype, grid, smem, dev, st);
   if (hp == 64)
-    return wide ? launch_score<kByte, 64, 256>(p, dtype, grid, smem, st)
-                : launch_score<kByte, 64, 64>(p, dtype, grid, smem, st);
-  return wide ? launch_score<kByte, 128, 256>(p, dtype, grid, smem, st)
-              : launch_score<kByte, 128, 128>(p, dtype, grid, smem, st);
+    return wide ? launch_score<kByte, 64, 256>(p, dtype, grid, smem, dev, st)
+                : launch_score<kByte, 64, 64>(p, dtype, grid, smem, dev, st);
+  return wide ? launch_score<kByte, 128, 256>(p, dtype, grid, smem, dev, st)
+              : launch_score<kByte, 128, 128>(p, dtype, grid, smem, dev, st);
 }
 
 }  // namespace
@@ -605,10 +606,8 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
     return DSEL_ERR_NULL;
   if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(keys) | reinterpret_cast<uintptr_t>(out)) & 15u) != 0)
     return DSEL_ERR_ALIGN;
-  if (const int st = check_device(); st != DSEL_OK) return st;
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return DSEL_ERR_CUDA;
+  if (const int st = current_device(&dev, &sms); st != DSEL_OK) return st;
 
   ScoreParams p = {};
   p.q = static_cast<const uint8_t*>(q);
@@ -678,6 +677,6 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
   p.items = int32_t(groups * p.chunks);
   const int grid = p.items < sms ? p.items : sms;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  return dtype == DSEL_E4M3 ? launch_heads<true>(p, dtype, hp, wide, grid, smem, cs)
-                            : launch_heads<false>(p, dtype, hp, wide, grid, smem, cs);
+  return dtype == DSEL_E4M3 ? launch_heads<true>(p, dtype, hp, wide, grid, smem, dev, cs)
+                            : launch_heads<false>(p, dtype, hp, wide, grid, smem, dev, cs);
 }

@@ -11,66 +11,72 @@ rules); this module checks the tensors and allocates the outputs.  Calls run on 
 tensors' device, on the current stream or on the raw handle given as ``stream``
 (outputs are then allocated for that stream).  Argument errors raise before any
 launch: ``TypeError`` / ``ValueError`` here, ``DselError`` from the library.
+
+Decoding steps call these with microseconds of work each, so the checks are few and
+plain, and the arguments go to the library packed into one array (``dsel_call``).
 """
 from __future__ import annotations
 
-from . import (DSEL_BF16, DSEL_E4M3, DSEL_F16, DSEL_F32, DSEL_I32, DSEL_I64, DSEL_OK, DselError, lib)
+import struct
+
+from . import (DSEL_BF16, DSEL_CALL_INDEX_SCORE, DSEL_CALL_LOGITS, DSEL_CALL_SPARSE_ATTN, DSEL_E4M3, DSEL_F16, DSEL_F32,
+               DSEL_I32, DSEL_I64, DSEL_OK, DselError, lib)
+
+# the arguments of the entry points, each in 8 bytes, in their order
+_LOGITS = struct.Struct("=25q")
+_SCORE = struct.Struct("=26q")
+_ATTN = struct.Struct("=30qd3q")
+
+_call = lib.dsel_call
+
 
 def _run(device, stream, call):
-    """``call(stream handle)`` with `device` current and, for a given stream, as torch's current one."""
+    """``call(stream handle)`` with CUDA device `device` current and, for a given stream, as torch's current one."""
     import torch
 
-    if stream is None and torch.cuda.current_device() == device.index:
-        return call(torch.cuda.current_stream(device).cuda_stream)
+    if stream is None and torch._C._cuda_getDevice() == device:
+        return call(torch._C._cuda_getCurrentRawStream(device))
     with torch.cuda.device(device):
         if stream is None:
-            return call(torch.cuda.current_stream(device).cuda_stream)
+            return call(torch._C._cuda_getCurrentRawStream(device))
         with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
             return call(stream)
 
 
-def _check(status):
-    if status != DSEL_OK:
-        raise DselError(status)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _vector(name, t, device, dtype, count):
-    """A contiguous 1-D tensor of `count` entries, or None."""
+    """The address of a contiguous 1-D tensor of `count` entries; 0 for None."""
     if t is None:
-        return None
-    if t.dtype != dtype or t.device != device or t.dim() != 1 or (count is not None and t.shape[0] != count):
-        raise ValueError(f"{name} must be a 1-D {dtype} tensor on {device}"
-                         + ("" if count is None else f" with {count} entries"))
+        return 0
+    if t.dtype is not dtype or t.get_device() != device or t.shape != (count,):
+        raise ValueError(f"{name} must be a 1-D {dtype} tensor on the same device with {count} entries")
     if not t.is_contiguous():   # a copy made here would run on another stream than the call
         raise ValueError(f"{name} must be contiguous")
-    return t
+    return t.data_ptr()
+
+
+def _rows_of(name, t, device, rows):
+    """Row stride of a 2-D tensor whose rows are contiguous and do not overlap."""
+    shape = t.shape
+    if len(shape) != 2 or t.get_device() != device or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} must be a 2-D tensor on the same device" + ("" if rows is None else f" with {rows} rows"))
+    stride, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if shape[0] <= 1:
+        return shape[1]
+    if stride < shape[1]:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return stride
 
 
 def _index_dtype(name, t):
     import torch
 
-    if t.dtype == torch.int32:
+    if t.dtype is torch.int32:
         return DSEL_I32
-    if t.dtype == torch.int64:
+    if t.dtype is torch.int64:
         return DSEL_I64
     raise TypeError(f"{name} must be int32 or int64")
-
-
-def _rows_of(name, t, device, rows):
-    """Row stride of a 2-D tensor whose rows are contiguous and do not overlap."""
-    if t.dim() != 2 or t.device != device or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be a 2-D tensor on {device}" + ("" if rows is None else f" with {rows} rows"))
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    if t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name} must have rows that do not overlap")
-    return t.stride(0)
 
 
 def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repetition=None, frequency=None,
@@ -92,68 +98,71 @@ def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repe
     """
     import torch
 
-    if logits.dim() != 2 or not logits.is_cuda:
+    f32, i32 = torch.float32, torch.int32
+    dev = logits.get_device()
+    if dev < 0 or logits.dim() != 2:
         raise ValueError("logits must be a 2-D CUDA tensor [rows, vocab] (there is no CPU path)")
-    if logits.dtype == torch.bfloat16:
+    if logits.dtype is torch.bfloat16:
         dt = DSEL_BF16
-    elif logits.dtype == torch.float32:
+    elif logits.dtype is f32:
         dt = DSEL_F32
     else:
         raise TypeError("logits must be bfloat16 or float32")
-    dev = logits.device
     rows, vocab = logits.shape
     if vocab < 1:
         raise ValueError("logits must have at least one column")
     x_stride = _rows_of("logits", logits, dev, None)
-    width = t_stride = 0
-    t_dt = DSEL_I32
+    p_tokens = t_dt = width = t_stride = 0
     if tokens is not None:
         t_dt = _index_dtype("tokens", tokens)
         t_stride = _rows_of("tokens", tokens, dev, rows)
         width = tokens.shape[1]
+        p_tokens = tokens.data_ptr()
     elif not (prompt_len is None and total_len is None and repetition is None and frequency is None
               and presence is None):
         raise ValueError("penalties and lengths need tokens=")
-    prompt_len = _vector("prompt_len", prompt_len, dev, torch.int32, rows)
-    total_len = _vector("total_len", total_len, dev, torch.int32, rows)
-    repetition = _vector("repetition", repetition, dev, torch.float32, rows)
-    frequency = _vector("frequency", frequency, dev, torch.float32, rows)
-    presence = _vector("presence", presence, dev, torch.float32, rows)
-    if not (bias_offsets is None) == (bias_ids is None) == (bias_values is None):
-        raise ValueError("bias_offsets, bias_ids and bias_values come together")
-    bias_count = 0
-    if bias_ids is not None:
-        bias_ids = _vector("bias_ids", bias_ids, dev, torch.int32, None)
-        bias_count = bias_ids.shape[0]
-        bias_values = _vector("bias_values", bias_values, dev, torch.float32, bias_count)
-        bias_offsets = _vector("bias_offsets", bias_offsets, dev, torch.int32, rows + 1)
-        if bias_count == 0:
-            bias_offsets = bias_ids = bias_values = None
-    m_stride = m_count = 0
+    p_prompt = _vector("prompt_len", prompt_len, dev, i32, rows)
+    p_total = _vector("total_len", total_len, dev, i32, rows)
+    p_rep = _vector("repetition", repetition, dev, f32, rows)
+    p_freq = _vector("frequency", frequency, dev, f32, rows)
+    p_pres = _vector("presence", presence, dev, f32, rows)
+    p_boff = p_bids = p_bval = n_bias = 0
+    if bias_ids is not None or bias_offsets is not None or bias_values is not None:
+        if bias_ids is None or bias_offsets is None or bias_values is None:
+            raise ValueError("bias_offsets, bias_ids and bias_values come together")
+        n_bias = bias_ids.shape[0] if bias_ids.dim() == 1 else -1
+        p_bids = _vector("bias_ids", bias_ids, dev, i32, n_bias)
+        p_bval = _vector("bias_values", bias_values, dev, f32, n_bias)
+        p_boff = _vector("bias_offsets", bias_offsets, dev, i32, rows + 1)
+        if n_bias == 0:
+            p_boff = p_bids = p_bval = 0
+    p_mask = m_stride = m_count = p_mrows = 0
     if mask is not None:
-        if mask.dtype != torch.int32:
+        if mask.dtype is not i32:
             raise TypeError("mask must be int32 words")
         m_stride = _rows_of("mask", mask, dev, None)
-        m_count = mask.shape[0]
-        mask_rows = _vector("mask_rows", mask_rows, dev, torch.int32, rows)
-        if mask.shape[1] * 32 < vocab:
+        m_count, words = mask.shape
+        p_mrows = _vector("mask_rows", mask_rows, dev, i32, rows)
+        if words * 32 < vocab:
             raise ValueError("mask rows must hold a bit for every token")
         if mask_rows is None and m_count < rows:
             raise ValueError("mask needs a row for every row of logits, or mask_rows=")
-        if m_count == 0:
-            mask = mask_rows = None
+        if m_count > 0:
+            p_mask = mask.data_ptr()
     elif mask_rows is not None:
         raise ValueError("mask_rows needs mask=")
-    if out is not None and (out.dtype != torch.float32 or out.device != dev or out.dim() != 2 or out.shape[0] != rows
+    if out is not None and (out.dtype is not f32 or out.get_device() != dev or out.dim() != 2 or out.shape[0] != rows
                             or out.shape[1] < vocab or out.shape[1] % 16 or not out.is_contiguous()):
         raise ValueError("out must be a contiguous float32 tensor [rows, n], n >= vocab a multiple of 16")
 
     def call(handle):
-        o = out if out is not None else torch.empty((rows, (vocab + 15) // 16 * 16), dtype=torch.float32, device=dev)
-        _check(lib.dsel_logits(logits.data_ptr(), dt, rows, vocab, x_stride, _ptr(tokens), t_dt, width, t_stride,
-                               _ptr(prompt_len), _ptr(total_len), _ptr(repetition), _ptr(frequency), _ptr(presence),
-                               _ptr(bias_offsets), _ptr(bias_ids), _ptr(bias_values), bias_count, _ptr(mask),
-                               m_stride, m_count, _ptr(mask_rows), o.data_ptr(), o.shape[1], handle))
+        o = out if out is not None else logits.new_empty((rows, vocab + 15 & ~15), dtype=f32)
+        status = _call(DSEL_CALL_LOGITS, _LOGITS.pack(
+            logits.data_ptr(), dt, rows, vocab, x_stride, p_tokens, t_dt, width, t_stride, p_prompt, p_total, p_rep,
+            p_freq, p_pres, p_boff, p_bids, p_bval, n_bias, p_mask, m_stride, m_count, p_mrows, o.data_ptr(),
+            o.shape[1], handle))
+        if status != DSEL_OK:
+            raise DselError(status)
         return o
 
     return _run(dev, stream, call)
@@ -163,33 +172,37 @@ def _operand_dtype(name, t, byte):
     """The DSEL code of a 16-bit operand (or, where `byte`, of an e4m3 one)."""
     import torch
 
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return DSEL_BF16
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return DSEL_F16
-    if byte and t.dtype == torch.float8_e4m3fn:
+    if byte and t.dtype is torch.float8_e4m3fn:
         return DSEL_E4M3
     raise TypeError(f"{name} must be bfloat16" + (", float16 or float8_e4m3fn" if byte else " or float16"))
 
 
 def _queries(q, table, end, seq_ids):
-    """Checks what every query of a paged cache comes with; (device, tokens, table stride)."""
+    """Checks what every query of a paged cache comes with: (device, tokens, table stride, address of end, of seq_ids)."""
     import torch
 
-    if q.dim() != 3 or not q.is_cuda:
+    dev = q.get_device()
+    if dev < 0 or q.dim() != 3:
         raise ValueError("q must be a 3-D CUDA tensor [tokens, heads, dim] (there is no CPU path)")
-    dev, tokens = q.device, q.shape[0]
-    if q.stride(2) != 1 and q.shape[2] > 1:
+    tokens = q.shape[0]
+    if q.stride(2) != 1:
         raise ValueError("q must be contiguous in its last dimension")
-    if table.dtype != torch.int32:
+    if table.dtype is not torch.int32:
         raise TypeError("block_table must be int32")
     t_stride = _rows_of("block_table", table, dev, None)
-    _vector("end", end, dev, torch.int32, tokens)
+    if end is None:
+        raise ValueError("end (the keys each query sees) must be given")
+    p_end = _vector("end", end, dev, torch.int32, tokens)
+    p_seq = 0
     if seq_ids is not None:
-        _vector("seq_ids", seq_ids, dev, torch.int32, tokens)
-    elif table.shape[0] not in (1, tokens):
+        p_seq = _vector("seq_ids", seq_ids, dev, torch.int32, tokens)
+    elif table.shape[0] != 1 and table.shape[0] != tokens:
         raise ValueError("block_table needs one row, or one for each query, or seq_ids=")
-    return dev, tokens, t_stride
+    return dev, tokens, t_stride, p_end, p_seq
 
 
 def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=None, row_stride=None, out_dtype=None,
@@ -209,41 +222,48 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
     """
     import torch
 
+    f32 = torch.float32
     dt = _operand_dtype("q", q, True)
-    dev, tokens, t_stride = _queries(q, block_table, end, seq_ids)
-    heads, dim = q.shape[1], q.shape[2]
-    if keys.dtype != q.dtype or keys.device != dev or keys.dim() != 3 or keys.shape[2] != dim or keys.stride(2) != 1:
+    dev, tokens, t_stride, p_end, p_seq = _queries(q, block_table, end, seq_ids)
+    _, heads, dim = q.shape
+    if (keys.dtype is not q.dtype or keys.get_device() != dev or keys.dim() != 3 or keys.shape[2] != dim
+            or keys.stride(2) != 1):
         raise ValueError("keys must be [pages, page_size, dim] of q's type on its device, contiguous in the last dimension")
-    if weights.dtype != torch.float32 or weights.shape[1:] != (heads,):
+    if weights.dtype is not f32 or weights.shape != (tokens, heads):
         raise ValueError("weights must be float32 [tokens, heads]")
     w_stride = _rows_of("weights", weights, dev, tokens)
-    pages, page = keys.shape[0], keys.shape[1]
-    s_stride = 0
+    pages, page, _ = keys.shape
+    k_page, k_row, _ = keys.stride()
+    p_scale = s_stride = 0
     if key_scale is not None:
-        if key_scale.dtype != torch.float32 or key_scale.shape != (pages, page):
+        if key_scale.dtype is not f32 or key_scale.shape != (pages, page):
             raise ValueError("key_scale must be float32 [pages, page_size]")
         s_stride = _rows_of("key_scale", key_scale, dev, pages)
+        p_scale = key_scale.data_ptr()
+    seqs, t_width = block_table.shape
     if out is not None:
-        if out.dim() != 2 or out.device != dev or out.shape[0] != tokens or not out.is_contiguous():
+        if out.dim() != 2 or out.get_device() != dev or out.shape[0] != tokens or not out.is_contiguous():
             raise ValueError("out must be a contiguous tensor [tokens, row_stride]")
-        if (row_stride is not None and out.shape[1] != row_stride) or (out_dtype is not None and out.dtype != out_dtype):
+        if (row_stride is not None and out.shape[1] != row_stride) or (out_dtype is not None and out.dtype is not out_dtype):
             raise ValueError("out must have the row_stride and out_dtype that are given")
         row_stride, out_dtype = out.shape[1], out.dtype
     else:
         if row_stride is None:
-            row_stride = (block_table.shape[1] * page + 15) // 16 * 16
+            row_stride = t_width * page + 15 & ~15
         if out_dtype is None:
             out_dtype = torch.bfloat16
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is not torch.bfloat16 and out_dtype is not f32:
         raise TypeError("scores are bfloat16 or float32")
 
     def call(handle):
-        o = out if out is not None else torch.empty((tokens, row_stride), dtype=out_dtype, device=dev)
-        _check(lib.dsel_index_score(q.data_ptr(), dt, tokens, heads, dim, q.stride(0), q.stride(1), weights.data_ptr(),
-                                    w_stride, keys.data_ptr(), pages, page, keys.stride(0), keys.stride(1),
-                                    _ptr(key_scale), s_stride, block_table.data_ptr(), block_table.shape[0],
-                                    block_table.shape[1], t_stride, _ptr(seq_ids), end.data_ptr(), o.data_ptr(),
-                                    DSEL_F32 if out_dtype == torch.float32 else DSEL_BF16, row_stride, handle))
+        o = out if out is not None else weights.new_empty((tokens, row_stride), dtype=out_dtype)
+        q_token, q_head, _ = q.stride()
+        status = _call(DSEL_CALL_INDEX_SCORE, _SCORE.pack(
+            q.data_ptr(), dt, tokens, heads, dim, q_token, q_head, weights.data_ptr(), w_stride, keys.data_ptr(),
+            pages, page, k_page, k_row, p_scale, s_stride, block_table.data_ptr(), seqs, t_width, t_stride, p_seq,
+            p_end, o.data_ptr(), DSEL_F32 if out_dtype is f32 else DSEL_BF16, row_stride, handle))
+        if status != DSEL_OK:
+            raise DselError(status)
         return o
 
     return _run(dev, stream, call)
@@ -267,39 +287,47 @@ def sparse_attention(q, k_cache, v_cache, block_table, indices, end, *, block=1,
     import torch
 
     dt = _operand_dtype("q", q, False)
-    dev, tokens, t_stride = _queries(q, block_table, end, seq_ids)
-    heads, dim = q.shape[1], q.shape[2]
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if c.dtype != q.dtype or c.device != dev or c.dim() != 4 or c.shape[3] != dim or c.stride(3) != 1:
-            raise ValueError(f"{name} must be [pages, page_size, kv_heads, dim] of q's type on its device, "
-                             "contiguous in the last dimension")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    pages, page, kv_heads = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
+    dev, tokens, t_stride, p_end, p_seq = _queries(q, block_table, end, seq_ids)
+    _, heads, dim = q.shape
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[3] != dim or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, kv_heads, dim], dim that of q")
+    if (k_cache.dtype is not q.dtype or v_cache.dtype is not q.dtype or k_cache.get_device() != dev
+            or v_cache.get_device() != dev):
+        raise ValueError("k_cache and v_cache must be of q's type on its device")
+    pages, page, kv_heads, _ = shape
+    k_page, k_row, k_head, k_step = k_cache.stride()
+    v_page, v_row, v_head, v_step = v_cache.stride()
+    if k_step != 1 or v_step != 1:
+        raise ValueError("k_cache and v_cache must be contiguous in their last dimension")
     i_dt = _index_dtype("indices", indices)
-    if indices.device != dev or indices.dim() not in (2, 3) or indices.shape[0] != tokens:
+    i_shape, i_stride = indices.shape, indices.stride()
+    if len(i_shape) not in (2, 3) or i_shape[0] != tokens or indices.get_device() != dev:
         raise ValueError("indices must be [tokens, k] or [tokens, kv_heads, k] on q's device")
-    if indices.dim() == 3 and indices.shape[1] != kv_heads:
+    if len(i_shape) == 3 and i_shape[1] != kv_heads:
         raise ValueError("indices must have one list, or one for each key head")
-    take = indices.shape[-1]
-    if take > 1 and indices.stride(-1) != 1:
+    take = i_shape[-1]
+    if take > 1 and i_stride[-1] != 1:
         raise ValueError("indices must be contiguous in the last dimension")
     if scale is None:
         scale = dim ** -0.5
-    if out is not None and (out.dtype != q.dtype or out.device != dev or out.shape != (tokens, heads, dim)
+    if out is not None and (out.dtype is not q.dtype or out.get_device() != dev or out.shape != (tokens, heads, dim)
                             or not out.is_contiguous()):
         raise ValueError("out must be a contiguous tensor of q's shape and type")
 
     def call(handle):
-        o = out if out is not None else torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
-        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
-        _check(lib.dsel_sparse_attn(q.data_ptr(), dt, tokens, heads, kv_heads, dim, q.stride(0), q.stride(1),
-                                    k_cache.data_ptr(), v_cache.data_ptr(), pages, page, *k_cache.stride()[:3],
-                                    *v_cache.stride()[:3], block_table.data_ptr(), block_table.shape[0],
-                                    block_table.shape[1], t_stride, _ptr(seq_ids), end.data_ptr(),
-                                    indices.data_ptr(), i_dt, take, indices.stride(0),
-                                    indices.stride(1) if indices.dim() == 3 else 0, block, scale, o.data_ptr(),
-                                    _ptr(lse), handle))
+        o = out if out is not None else q.new_empty((tokens, heads, dim))
+        lse = q.new_empty((tokens, heads), dtype=torch.float32) if return_lse else None
+        q_token, q_head, _ = q.stride()
+        seqs, t_width = block_table.shape
+        status = _call(DSEL_CALL_SPARSE_ATTN, _ATTN.pack(
+            q.data_ptr(), dt, tokens, heads, kv_heads, dim, q_token, q_head, k_cache.data_ptr(), v_cache.data_ptr(),
+            pages, page, k_page, k_row, k_head, v_page, v_row, v_head, block_table.data_ptr(), seqs, t_width,
+            t_stride, p_seq, p_end, indices.data_ptr(), i_dt, take, i_stride[0],
+            i_stride[1] if len(i_shape) == 3 else 0, block, scale, o.data_ptr(),
+            0 if lse is None else lse.data_ptr(), handle))
+        if status != DSEL_OK:
+            raise DselError(status)
         return (o, lse) if return_lse else o
 
     return _run(dev, stream, call)
