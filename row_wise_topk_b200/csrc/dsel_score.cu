@@ -136,14 +136,32 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
+// N columns of this warp's lanes; the values may be used after tmem_wait<N> on the same array.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r);
+template <>
+__device__ __forceinline__ void tmem_load<16>(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr));
 }
-__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+template <>
+__device__ __forceinline__ void tmem_load<32>(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(addr));
+}
+// (the registers are operands, so that no use of them moves ahead of the wait)
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t* r);
+template <>
+__device__ __forceinline__ void tmem_wait<16>(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+template <>
+__device__ __forceinline__ void tmem_wait<32>(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
 __device__ __forceinline__ float relu(float x) {   // a NaN stays one
   float y;
   asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
@@ -215,13 +233,18 @@ __device__ __forceinline__ Run load_run(const ScoreParams& p, const Item& it, in
   return r;
 }
 
-__device__ __forceinline__ int64_t key_slot(const ScoreParams& p, const int32_t* table, int32_t pos, int32_t* page_out) {
-  const int32_t i = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
-  int32_t page = -1;
-  if (i < p.table_width) page = table[i];
-  if (page < 0 || page >= p.pages) page = -1;
-  *page_out = page;
-  return pos - i * p.page_size;
+// Where a key lies: its page as the table gives it (-1: none), and its place in the page.
+struct KeyPage {
+  int32_t page, place;
+};
+__device__ __forceinline__ KeyPage fetch_page(const ScoreParams& p, const int32_t* table, int32_t pos, int32_t end) {
+  KeyPage at = {-1, 0};
+  if (pos < end) {
+    const int32_t i = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
+    at.place = pos - i * p.page_size;
+    if (i < p.table_width) at.page = table[i];
+  }
+  return at;
 }
 
 // kByte: e4m3 operands.  kHeads: heads per query, padded.  kCols: columns of an accumulator.
@@ -303,64 +326,76 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
         const int lo = run.a > first ? run.a : first;
         const int hi = run.b < first + kPerTile ? run.b : first + kPerTile;
         const int32_t* table = p.table + int64_t(run.seq < 0 ? 0 : run.seq) * p.table_stride;
-        for (int32_t k = 0; k < run.tiles; ++k) {
-          const bool mine = p.col_tiles == 2 ? lo < hi : int(turn & 1u) == b;
-          ++turn;
-          if (!mine) continue;
-          // the key's page and scale, while the product runs
+        // each key's page is fetched a tile of this warpgroup ahead of its use
+        const int skip = p.col_tiles == 2 ? 1 : 2;
+        int32_t k = p.col_tiles == 2 ? 0 : int32_t((turn & 1u) != uint32_t(b));
+        turn += uint32_t(run.tiles);
+        if (lo >= hi) k = run.tiles;
+        KeyPage next = fetch_page(p, table, (it.tile0 + k) * kTile + row, k < run.tiles ? run.end : 0);
+        for (; k < run.tiles; k += skip) {
           const int32_t pos = (it.tile0 + k) * kTile + row;
-          bool live = pos < run.end;
+          const KeyPage at = next;
+          next = fetch_page(p, table, pos + skip * kTile, k + skip < run.tiles ? run.end : 0);
+          const bool live = at.page >= 0 && at.page < p.pages;
           float scale = 1.f;
-          if (live) {
-            int32_t page;
-            const int64_t at = key_slot(p, table, pos, &page);
-            live = page >= 0;
-            if (live && p.key_scale != nullptr) scale = p.key_scale[int64_t(page) * p.scale_page_stride + at];
-          }
+          if (p.key_scale != nullptr && live) scale = p.key_scale[int64_t(at.page) * p.scale_page_stride + at.place];
           if (!bar_wait(done0 + 8 * b, uses & 1u)) {
             ok = false;
             break;
           }
           ++uses;
           tc_fence_after();
-          for (int qi = lo; qi < hi; ++qi) {
-            const int c0 = (qi - first) * kHeads;
-            uint64_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;   // four pairs of sums, to shorten the chains
+          // the columns of the run's queries in pieces, the next piece on its way while one is summed
+          constexpr int kPiece = kHeads < 32 ? kHeads : 32;
+          constexpr int kPieces = kHeads / kPiece;
+          uint32_t xa[kPiece], xb[kPiece];
+          uint64_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;   // four pairs of sums, to shorten the chains
+          int i = (lo - first) * kPieces;
+          const int n = (hi - first) * kPieces;
+          auto piece = [&](uint32_t* x, uint32_t* y) {
+            tmem_wait<kPiece>(x);
+            if (i + 1 < n) {
+              tmem_load<kPiece>(acc + uint32_t((i + 1) * kPiece), y);
+            } else {   // nothing of the accumulator is left to read
+              tc_fence_before();
+              bar_arrive(free0 + 8 * b);
+            }
+            const int c = (i % kPieces) * kPiece;   // first head of the piece
+            if (c + kPiece > p.heads) {   // columns behind the last head count for nothing, whatever they hold
 #pragma unroll
-            for (int c = 0; c < kHeads; c += 16) {
-              uint32_t x[16];
-              tmem_load16(acc + uint32_t(c0 + c), x);
-              tmem_wait();
-              if (c < p.heads) {
-                if (c + 16 > p.heads) {   // columns behind the last head count for nothing, whatever they hold
+              for (int j = 0; j < kPiece; ++j)
+                if (c + j >= p.heads) x[j] = 0u;
+            }
+            const ulonglong2* w2 = reinterpret_cast<const ulonglong2*>(w + i * kPiece);
 #pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    if (c + i >= p.heads) x[i] = 0u;
-                }
-                const ulonglong2* w2 = reinterpret_cast<const ulonglong2*>(w + c0 + c);
-#pragma unroll
-                for (int i = 0; i < 16; i += 8) {
-                  const ulonglong2 wa = w2[i / 4], wb = w2[i / 4 + 1];
-                  s0 = fma2(pack2(relu(__uint_as_float(x[i + 0])), relu(__uint_as_float(x[i + 1]))), wa.x, s0);
-                  s1 = fma2(pack2(relu(__uint_as_float(x[i + 2])), relu(__uint_as_float(x[i + 3]))), wa.y, s1);
-                  s2 = fma2(pack2(relu(__uint_as_float(x[i + 4])), relu(__uint_as_float(x[i + 5]))), wb.x, s2);
-                  s3 = fma2(pack2(relu(__uint_as_float(x[i + 6])), relu(__uint_as_float(x[i + 7]))), wb.y, s3);
-                }
+            for (int j = 0; j < kPiece; j += 8) {
+              const ulonglong2 wa = w2[j / 4], wb = w2[j / 4 + 1];
+              s0 = fma2(pack2(relu(__uint_as_float(x[j + 0])), relu(__uint_as_float(x[j + 1]))), wa.x, s0);
+              s1 = fma2(pack2(relu(__uint_as_float(x[j + 2])), relu(__uint_as_float(x[j + 3]))), wa.y, s1);
+              s2 = fma2(pack2(relu(__uint_as_float(x[j + 4])), relu(__uint_as_float(x[j + 5]))), wb.x, s2);
+              s3 = fma2(pack2(relu(__uint_as_float(x[j + 6])), relu(__uint_as_float(x[j + 7]))), wb.y, s3);
+            }
+            if (i % kPieces == kPieces - 1) {   // the query's last
+              const int qi = first + i / kPieces;
+              const int32_t end = __shfl_sync(0xFFFFFFFFu, it.end, qi);
+              float v = ((sum2(s0) + sum2(s1)) + (sum2(s2) + sum2(s3))) * scale;
+              if (!live || pos >= end) v = -__int_as_float(0x7F800000);
+              if (pos < p.row_stride) {
+                const int64_t o = int64_t(it.token0 + qi) * p.row_stride + pos;
+                if (p.out_f32)
+                  static_cast<float*>(p.out)[o] = v;
+                else
+                  static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
               }
+              s0 = s1 = s2 = s3 = 0;
             }
-            const int32_t end = __shfl_sync(0xFFFFFFFFu, it.end, qi);
-            float v = ((sum2(s0) + sum2(s1)) + (sum2(s2) + sum2(s3))) * scale;
-            if (!live || pos >= end) v = -__int_as_float(0x7F800000);
-            if (pos < p.row_stride) {
-              const int64_t o = int64_t(it.token0 + qi) * p.row_stride + pos;
-              if (p.out_f32)
-                static_cast<float*>(p.out)[o] = v;
-              else
-                static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
-            }
+            ++i;
+          };
+          tmem_load<kPiece>(acc + uint32_t(i * kPiece), xa);
+          while (i < n) {
+            piece(xa, xb);
+            if (i < n) piece(xb, xa);
           }
-          tc_fence_before();
-          bar_arrive(free0 + 8 * b);
         }
         // -inf behind the run's last tile (both warpgroups' threads, 16 bytes each)
         const int64_t from = pos0 + int64_t(run.tiles) * kTile;
@@ -378,6 +413,7 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     const int pw = warp - kEpiWarps;
     const int tid = pw * 32 + lane;
     const int per_row = p.row_bytes / 16;   // 16-byte pieces of a key
+    const int per_shift = (per_row & (per_row - 1)) == 0 ? __ffs(per_row) - 1 : -1;
     uint32_t issued = 0, told = 0;          // tiles whose copies were started; tiles announced as complete
     uint32_t n_item = 0;                    // items that had a tile
     bool ok = true;
@@ -397,15 +433,11 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
         const Run run = load_run(p, it, a);
         a = run.b;
         const int32_t* table = p.table + int64_t(run.seq < 0 ? 0 : run.seq) * p.table_stride;
+        // each thread looks up one key of a tile, a tile ahead of its use
+        KeyPage next = fetch_page(p, table, it.tile0 * kTile + tid, run.tiles > 0 ? run.end : 0);
         for (int32_t k = 0; k < run.tiles; ++k) {
-          // this thread's key of the tile: where it lies
-          const int32_t pos = (it.tile0 + k) * kTile + tid;
-          int64_t off = -1;
-          if (pos < run.end) {
-            int32_t page;
-            const int64_t at = key_slot(p, table, pos, &page);
-            if (page >= 0) off = int64_t(page) * p.page_bytes + at * p.key_bytes;
-          }
+          const KeyPage at = next;
+          next = fetch_page(p, table, (it.tile0 + k + 1) * kTile + tid, k + 1 < run.tiles ? run.end : 0);
           if (!queries) {
             const uint32_t buf = n_item % uint32_t(p.q_bufs), use = n_item / uint32_t(p.q_bufs);
             if (use > 0) {
@@ -437,15 +469,27 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
             ok = false;
             break;
           }
-          const uint32_t dst0 = ring0 + slot * stage_bytes;
+          const int64_t off = at.page >= 0 && at.page < p.pages
+                                  ? int64_t(at.page) * p.page_bytes + int64_t(at.place) * p.key_bytes
+                                  : -1;
+          const uint32_t dst0 = ring0 + slot * stage_bytes + uint32_t(pw) * (32 * 128);
           // each warp brings its own 32 keys, consecutive lanes consecutive pieces
-          for (int i = lane; i < 32 * per_row; i += 32) {
-            const int r = i / per_row, piece = i - r * per_row;
-            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
-            const int rr = pw * 32 + r;
-            const uint32_t dst = dst0 + uint32_t(piece >> 3) * kPanel + uint32_t(rr) * 128u +
-                                 (uint32_t((piece & 7) ^ (rr & 7)) << 4);
-            copy16(dst, p.keys + (o < 0 ? 0 : o + piece * 16), o >= 0);
+          if (per_shift >= 0) {
+            const int piece = lane & (per_row - 1), rows = 32 >> per_shift;
+            const uint32_t to = dst0 + uint32_t(piece >> 3) * kPanel;
+            const uint8_t* from = p.keys + piece * 16;
+#pragma unroll 4
+            for (int r = lane >> per_shift; r < 32; r += rows) {
+              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+              copy16(to + uint32_t(r) * 128u + (uint32_t((piece ^ r) & 7) << 4), from + (o < 0 ? 0 : o), o >= 0);
+            }
+          } else {
+            for (int i = lane; i < 32 * per_row; i += 32) {
+              const int r = i / per_row, piece = i - r * per_row;
+              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+              copy16(dst0 + uint32_t(piece >> 3) * kPanel + uint32_t(r) * 128u + (uint32_t((piece ^ r) & 7) << 4),
+                     p.keys + (o < 0 ? 0 : o + piece * 16), o >= 0);
+            }
           }
           copy_commit();
           ++issued;
