@@ -12,16 +12,17 @@
 // What bounds it: one query per sequence (decoding) reads 2 * dim bytes of key for
 // 2 * heads * dim operations: HBM.  A chunk of queries over the same keys is bound by
 // the tensor cores (2 * heads * dim operations per score), beside which the sum over
-// heads costs 1.75 issue slots per (key, head): the epilogue of one accumulator runs
+// heads costs 1.5 instructions per (key, head): the epilogue of one accumulator runs
 // under the products of the other.
 //
 // Roles of a persistent CTA: 8 warps read accumulators, sum over heads and store
-// (warpgroup b owns accumulator b), 4 warps bring key tiles and queries with 16-byte
-// asynchronous copies (pages may end anywhere, so each key is addressed through the
-// page table by itself; a tensor-map box would need pages of a fixed power of two),
-// one warp issues the products.
+// (warpgroup b owns accumulator b), one warp brings key tiles and queries by TMA, one
+// issues the products.  Pages of a power of two of at least 8 keys are boxes of a
+// tensor map; pages of other sizes end anywhere in a tile, so there two warps address
+// each key by itself and copy it in 16-byte pieces.
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -36,8 +37,9 @@ __device__ int g_score_status;   // DSEL_ERR_DEVICE_TIMEOUT when a wait gave up
 constexpr int kTile = 128;            // keys per tile (TMEM lanes)
 constexpr int kPanel = kTile * 128;   // a tile's panel: 128 rows of 128 bytes, 128-byte swizzle
 constexpr int kEpiWarps = 8;
-constexpr int kProdWarps = 4;
+constexpr int kProdWarps = 2;
 constexpr int kProdThreads = kProdWarps * 32;
+constexpr int kProdKeys = kTile / kProdWarps;   // keys of a tile that a copying warp brings
 constexpr int kScThreads = (kEpiWarps + kProdWarps + 1) * 32;
 constexpr int kMaxRing = 8;
 constexpr int kScoreSmem = 227 * 1024;   // all of a CTA's shared memory
@@ -45,8 +47,9 @@ constexpr int kBarBytes = 256;          // the barriers and the accumulators' ad
 constexpr uint64_t kWaitLimit = 2000000000ull;   // 2 s
 
 struct ScoreParams {
-  const uint8_t* q;
-  int64_t q_token_bytes, q_head_bytes;
+  CUtensorMap q_map;      // [tokens][heads][dim], boxes of one accumulator's queries, 128 bytes of depth
+  CUtensorMap key_map;    // [pages][page_size][dim], boxes of box_keys keys; used where box_keys > 0
+  int32_t box_keys;       // keys of a box: the page, or a tile of a longer one; 0: keys are copied one by one
   const float* weights;
   int64_t weights_stride;
   const uint8_t* keys;
@@ -63,7 +66,7 @@ struct ScoreParams {
   int32_t seqs, table_width;
   int32_t tokens, heads, row_bytes;       // row_bytes: dim * element size
   int32_t col_tiles;                      // accumulators per key tile: 1 or 2
-  int32_t ring, lag;                      // key tiles in shared memory; copies in flight before the oldest is awaited
+  int32_t ring, lag;                      // key tiles in shared memory; copied tiles in flight before the oldest is awaited
   int32_t q_bufs;                         // query buffers
   int32_t chunk;                          // key tiles per work item
   int32_t chunks, items;
@@ -108,6 +111,16 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
   return bar_try(bar, parity) || bar_wait_slow(bar, parity);
 }
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -136,51 +149,58 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// N columns of this warp's lanes; the values may be used after tmem_wait<N> on the same array.
+// A fragment of 16 keys (TMEM lanes) and 8 * N columns: in group j of 8 columns a thread gets
+// columns 2 (lane % 4) and the next of keys lane / 4 (r[4j], r[4j + 1]) and lane / 4 + 8.  The
+// values may be used after tmem_wait<N> on the same array.
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t* r);
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t* r);   // (the registers are operands: no use moves ahead of it)
 template <>
-__device__ __forceinline__ void tmem_load<16>(uint32_t addr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+__device__ __forceinline__ void tmem_load<2>(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+template <>
+__device__ __forceinline__ void tmem_wait<2>(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+}
+template <>
+__device__ __forceinline__ void tmem_load<4>(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                : "r"(addr));
 }
 template <>
-__device__ __forceinline__ void tmem_load<32>(uint32_t addr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-               : "r"(addr));
-}
-// (the registers are operands, so that no use of them moves ahead of the wait)
-template <int N>
-__device__ __forceinline__ void tmem_wait(uint32_t* r);
-template <>
-__device__ __forceinline__ void tmem_wait<16>(uint32_t* r) {
+__device__ __forceinline__ void tmem_wait<4>(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 template <>
-__device__ __forceinline__ void tmem_wait<32>(uint32_t* r) {
+__device__ __forceinline__ void tmem_load<8>(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(addr));
+}
+template <>
+__device__ __forceinline__ void tmem_wait<8>(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
-__device__ __forceinline__ float relu(float x) {   // a NaN stays one
+__device__ __forceinline__ float relu(uint32_t x) {   // a NaN stays one
   float y;
-  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(__uint_as_float(x)));
   return y;
 }
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+
+// a * b + c of two floats in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float sum2(uint64_t a) {
-  float x, y;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
-  return x + y;
 }
 
 // A work item: up to 32 consecutive queries (one per lane) and a range of key tiles.
@@ -248,7 +268,8 @@ __device__ __forceinline__ KeyPage fetch_page(const ScoreParams& p, const int32_
 }
 
 // kByte: e4m3 operands.  kHeads: heads per query, padded.  kCols: columns of an accumulator.
-template <bool kByte, int kHeads, int kCols>
+// kFull: no head is padding (the test for it would cost the sum as much as its arithmetic).
+template <bool kByte, int kHeads, int kCols, bool kFull>
 __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_constant__ ScoreParams p,
                                                              const uint32_t idesc) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -260,13 +281,13 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
   const uint32_t q_panel = uint32_t(kCols) * 128u;                       // one accumulator's queries, one panel
   const uint32_t q_bytes = uint32_t(p.col_tiles * panels) * q_panel;     // one query buffer
   uint8_t* tail = smem + p.ring * stage_bytes + p.q_bufs * q_bytes;
-  float* wsm = reinterpret_cast<float*>(tail);                           // [2][kCols] weights
-  const uint32_t full0 = shared_addr(tail + 2 * kCols * 4), empty0 = full0 + 8 * kMaxRing;
-  const uint32_t done0 = full0 + 16 * kMaxRing, free0 = done0 + 16, qfree0 = free0 + 16;
+  const uint32_t full0 = shared_addr(tail), empty0 = full0 + 8 * kMaxRing;
+  const uint32_t done0 = full0 + 16 * kMaxRing, free0 = done0 + 16, qfull0 = free0 + 16,
+                 qfree0 = qfull0 + 16;
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
   const int per_item = kPerTile * p.col_tiles;
-  static_assert((2 * kMaxRing + 6) * 8 + 8 <= kBarBytes, "barriers outgrew their reservation");
-  uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(tail + 2 * kCols * 4 + (2 * kMaxRing + 6) * 8);
+  static_assert((2 * kMaxRing + 8) * 8 + 8 <= kBarBytes, "barriers outgrew their reservation");
+  uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(tail + (2 * kMaxRing + 8) * 8);
   if ((ring0 & 1023u) != 0u) {   // the swizzled panels need it; the dynamic window starts aligned when it is alone
     if (threadIdx.x == 0) atomicExch(&g_score_status, DSEL_ERR_ALIGN);
     return;
@@ -274,12 +295,13 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.ring; ++i) {
-      bar_init(full0 + 8 * i, kProdThreads);
+      bar_init(full0 + 8 * i, p.box_keys > 0 ? 1 : kProdThreads);
       bar_init(empty0 + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(done0 + 8 * i, 1);
       bar_init(free0 + 8 * i, 128);
+      bar_init(qfull0 + 8 * i, 1);
       bar_init(qfree0 + 8 * i, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -301,22 +323,22 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
   if (warp < kEpiWarps) {
     // ---------------- sum over heads, stores ----------------
     const int b = warp >> 2;                       // warpgroup and accumulator
-    const int row = int(threadIdx.x & 127);        // key of the tile
+    const int row = (warp & 3) * 32 + (lane >> 2) + (lane & 3) * 8;   // the key of a tile whose sum ends up here
     const uint32_t acc = tmem + uint32_t(b * kCols) + (uint32_t(warp & 3) << 21);   // lane quarter in bits 16..
-    float* w = wsm + b * kCols;
     uint32_t uses = 0;    // times this accumulator was filled
     uint32_t turn = 0;    // key tiles so far (col_tiles == 1: accumulators take turns)
     bool ok = true;
-    // (a wait that gave up ends the work, not the loop: every warp passes the same barriers)
-    for (int32_t item = int32_t(blockIdx.x); item < p.items; item += int32_t(gridDim.x)) {
+    for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
       const Item it = load_item(p, item, per_item);
       const int first = p.col_tiles == 2 ? b * kPerTile : 0;   // the queries of this warpgroup's columns
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + b) : "memory");   // the last item's weights are no longer read
-      for (int i = row; i < kCols; i += 128) {
-        const int qi = first + i / kHeads, h = i % kHeads;
+      // the weights of this thread's columns
+      float w[kCols / 4];
+#pragma unroll
+      for (int i = 0; i < kCols / 4; ++i) {
+        const int col = (i >> 1) * 8 + (lane & 3) * 2 + (i & 1);
+        const int qi = first + col / kHeads, h = col % kHeads;
         w[i] = qi < it.count && h < p.heads ? p.weights[int64_t(it.token0 + qi) * p.weights_stride + h] : 0.f;
       }
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + b) : "memory");
       const int64_t pos0 = int64_t(it.tile0) * kTile;
       const int64_t pos_end = pos0 + int64_t(p.chunk) * kTile < p.row_stride ? pos0 + int64_t(p.chunk) * kTile : p.row_stride;
       for (int a = 0; a < it.count && ok;) {
@@ -345,56 +367,61 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
           }
           ++uses;
           tc_fence_after();
-          // the columns of the run's queries in pieces, the next piece on its way while one is summed
-          constexpr int kPiece = kHeads < 32 ? kHeads : 32;
-          constexpr int kPieces = kHeads / kPiece;
-          uint32_t xa[kPiece], xb[kPiece];
-          uint64_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;   // four pairs of sums, to shorten the chains
-          int i = (lo - first) * kPieces;
-          const int n = (hi - first) * kPieces;
-          auto piece = [&](uint32_t* x, uint32_t* y) {
-            tmem_wait<kPiece>(x);
-            if (i + 1 < n) {
-              tmem_load<kPiece>(acc + uint32_t((i + 1) * kPiece), y);
-            } else {   // nothing of the accumulator is left to read
+          // up to 64 columns at a time (one query's heads, or those of several) of all 32 keys
+          constexpr int kChunk = kCols < 64 ? kCols : 64;
+          constexpr int kGroups = kChunk / 8;
+          constexpr int kPerQuery = kHeads < kChunk ? kHeads : kChunk;
+          const int c_lo = (lo - first) * kHeads / kChunk, c_hi = ((hi - first) * kHeads + kChunk - 1) / kChunk;
+          float2 s[4];   // sums of keys lane / 4 + 8 j, even and odd columns
+#pragma unroll
+          for (int c = 0; c < kCols / kChunk; ++c) {
+            if (c < c_lo || c >= c_hi) continue;
+            uint32_t x[2][4 * kGroups];
+            tmem_load<kGroups>(acc + uint32_t(c * kChunk), x[0]);
+            tmem_load<kGroups>(acc + (16u << 16) + uint32_t(c * kChunk), x[1]);
+            tmem_wait<kGroups>(x[0]);
+            tmem_wait<kGroups>(x[1]);
+            if (c == c_hi - 1) {   // nothing of the accumulator is left to read
               tc_fence_before();
               bar_arrive(free0 + 8 * b);
             }
-            const int c = (i % kPieces) * kPiece;   // first head of the piece
-            if (c + kPiece > p.heads) {   // columns behind the last head count for nothing, whatever they hold
 #pragma unroll
-              for (int j = 0; j < kPiece; ++j)
-                if (c + j >= p.heads) x[j] = 0u;
-            }
-            const ulonglong2* w2 = reinterpret_cast<const ulonglong2*>(w + i * kPiece);
+            for (int q = 0; q < kChunk / kPerQuery; ++q) {
+              if (c * kChunk % kHeads == 0) s[0] = s[1] = s[2] = s[3] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < kPiece; j += 8) {
-              const ulonglong2 wa = w2[j / 4], wb = w2[j / 4 + 1];
-              s0 = fma2(pack2(relu(__uint_as_float(x[j + 0])), relu(__uint_as_float(x[j + 1]))), wa.x, s0);
-              s1 = fma2(pack2(relu(__uint_as_float(x[j + 2])), relu(__uint_as_float(x[j + 3]))), wa.y, s1);
-              s2 = fma2(pack2(relu(__uint_as_float(x[j + 4])), relu(__uint_as_float(x[j + 5]))), wb.x, s2);
-              s3 = fma2(pack2(relu(__uint_as_float(x[j + 6])), relu(__uint_as_float(x[j + 7]))), wb.y, s3);
-            }
-            if (i % kPieces == kPieces - 1) {   // the query's last
-              const int qi = first + i / kPieces;
-              const int32_t end = __shfl_sync(0xFFFFFFFFu, it.end, qi);
-              float v = ((sum2(s0) + sum2(s1)) + (sum2(s2) + sum2(s3))) * scale;
-              if (!live || pos >= end) v = -__int_as_float(0x7F800000);
-              if (pos < p.row_stride) {
-                const int64_t o = int64_t(it.token0 + qi) * p.row_stride + pos;
-                if (p.out_f32)
-                  static_cast<float*>(p.out)[o] = v;
-                else
-                  static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+              for (int j = q * kPerQuery / 8; j < (q + 1) * kPerQuery / 8; ++j) {
+                const float2 wj = make_float2(w[(c * kGroups + j) * 2], w[(c * kGroups + j) * 2 + 1]);
+#pragma unroll
+                for (int k4 = 0; k4 < 4; ++k4) {
+                  const uint32_t* xe = &x[k4 >> 1][4 * j + 2 * (k4 & 1)];
+                  float2 y = make_float2(relu(xe[0]), relu(xe[1]));
+                  if (!kFull) {   // columns behind the last head count for nothing, whatever they hold
+                    const int h = (c * kChunk + j * 8) % kHeads + (lane & 3) * 2;
+                    if (h >= p.heads) y.x = 0.f;
+                    if (h + 1 >= p.heads) y.y = 0.f;
+                  }
+                  s[k4] = fma2(y, wj, s[k4]);
+                }
               }
-              s0 = s1 = s2 = s3 = 0;
+              if (kHeads <= kChunk || (c + 1) * kChunk % kHeads == 0) {   // the query's last columns
+                // four sums in each of four lanes: every lane ends up with one key's
+                const float v0 = s[0].x + s[0].y, v1 = s[1].x + s[1].y, v2 = s[2].x + s[2].y, v3 = s[3].x + s[3].y;
+                const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
+                const float a0 = (odd ? v1 : v0) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+                const float a1 = (odd ? v3 : v2) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v2 : v3, 1);
+                float v = ((high ? a1 : a0) + __shfl_xor_sync(0xFFFFFFFFu, high ? a0 : a1, 2)) * scale;
+                const int qi = first + (c * kChunk + q * kPerQuery) / kHeads;
+                const int32_t end = __shfl_sync(0xFFFFFFFFu, it.end, qi & 31);
+                if (!live || pos >= end) v = -__int_as_float(0x7F800000);
+                if (qi >= lo && qi < hi && pos < p.row_stride) {
+                  const int64_t o = int64_t(it.token0 + qi) * p.row_stride + pos;
+                  if (p.out_f32)
+                    static_cast<float*>(p.out)[o] = v;
+                  else
+                    static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+                }
+              }
             }
-            ++i;
-          };
-          tmem_load<kPiece>(acc + uint32_t(i * kPiece), xa);
-          while (i < n) {
-            piece(xa, xb);
-            if (i < n) piece(xb, xa);
           }
         }
         // -inf behind the run's last tile (both warpgroups' threads, 16 bytes each)
@@ -411,13 +438,10 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
   } else if (warp < kEpiWarps + kProdWarps) {
     // ---------------- key tiles and queries ----------------
     const int pw = warp - kEpiWarps;
-    const int tid = pw * 32 + lane;
-    const int per_row = p.row_bytes / 16;   // 16-byte pieces of a key
-    const int per_shift = (per_row & (per_row - 1)) == 0 ? __ffs(per_row) - 1 : -1;
-    uint32_t issued = 0, told = 0;          // tiles whose copies were started; tiles announced as complete
-    uint32_t n_item = 0;                    // items that had a tile
+    uint32_t issued = 0, told = 0;   // tiles whose copies were started; copied tiles announced as complete
+    uint32_t n_item = 0;             // items that had a tile
     bool ok = true;
-    auto tell = [&]() {   // announce the oldest tile that is not yet: its copies are complete, and visible to the products
+    auto tell = [&]() {   // announce the oldest copied tile that is not yet: it is complete, and visible to the products
       fence_async_shared();
       bar_arrive(full0 + 8 * (told % uint32_t(p.ring)));
       ++told;
@@ -426,88 +450,139 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
       copy_wait<0>();
       while (told < issued) tell();
     };
-    for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
-      const Item it = load_item(p, item, per_item);
-      bool queries = false;   // loaded for this item
-      for (int a = 0; a < it.count && ok;) {
-        const Run run = load_run(p, it, a);
-        a = run.b;
-        const int32_t* table = p.table + int64_t(run.seq < 0 ? 0 : run.seq) * p.table_stride;
-        // each thread looks up one key of a tile, a tile ahead of its use
-        KeyPage next = fetch_page(p, table, it.tile0 * kTile + tid, run.tiles > 0 ? run.end : 0);
-        for (int32_t k = 0; k < run.tiles; ++k) {
-          const KeyPage at = next;
-          next = fetch_page(p, table, (it.tile0 + k + 1) * kTile + tid, k + 1 < run.tiles ? run.end : 0);
-          if (!queries) {
-            const uint32_t buf = n_item % uint32_t(p.q_bufs), use = n_item / uint32_t(p.q_bufs);
-            if (use > 0) {
-              // the products that read this buffer may still wait for tiles not yet announced
-              if (!bar_try(qfree0 + 8 * buf, (use - 1) & 1u)) flush();
-              if (!bar_wait(qfree0 + 8 * buf, (use - 1) & 1u)) {
+    // the item's queries, before its first tile
+    auto load_queries = [&](const Item& it) {
+      const uint32_t buf = n_item % uint32_t(p.q_bufs), use = n_item / uint32_t(p.q_bufs);
+      ++n_item;
+      if (pw != 0) return true;
+      if (use > 0) {
+        // the products that read this buffer may still wait for tiles not yet announced
+        if (p.box_keys == 0 && !__all_sync(0xFFFFFFFFu, bar_try(qfree0 + 8 * buf, (use - 1) & 1u))) flush();
+        if (!bar_wait(qfree0 + 8 * buf, (use - 1) & 1u)) return false;
+      }
+      if (lane == 0) {
+        bar_expect(qfull0 + 8 * buf, q_bytes);
+        for (int n = 0; n < p.col_tiles; ++n)
+          for (int i = 0; i < panels; ++i)
+            tma_load(q0 + buf * q_bytes + uint32_t(n * panels + i) * q_panel, &p.q_map, qfull0 + 8 * buf,
+                     i * (kByte ? 128 : 64), 0, it.token0 + n * kPerTile);
+      }
+      __syncwarp();
+      return true;
+    };
+    if (p.box_keys > 0) {
+      if (pw == 0) {
+        // lane i brings the tile's page i (or its part of a longer page); pages are looked up a tile ahead
+        const int boxes = kTile / p.box_keys;
+        const uint32_t box_bytes = uint32_t(p.box_keys) * 128u;
+        for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
+          const Item it = load_item(p, item, per_item);
+          bool queries = false;   // loaded for this item
+          for (int a = 0; a < it.count && ok;) {
+            const Run run = load_run(p, it, a);
+            a = run.b;
+            const int32_t* table = p.table + int64_t(run.seq < 0 ? 0 : run.seq) * p.table_stride;
+            const int32_t mine = it.tile0 * kTile + lane * p.box_keys;
+            KeyPage next = fetch_page(p, table, mine, lane < boxes && run.tiles > 0 ? run.end : 0);
+            for (int32_t k = 0; k < run.tiles; ++k) {
+              const KeyPage at = next;
+              const int32_t pos = mine + k * kTile;
+              next = fetch_page(p, table, pos + kTile, lane < boxes && k + 1 < run.tiles ? run.end : 0);
+              if (!queries) {
+                queries = true;
+                if (!load_queries(it)) {
+                  ok = false;
+                  break;
+                }
+              }
+              const uint32_t slot = issued % uint32_t(p.ring), round = issued / uint32_t(p.ring);
+              if (round > 0 && !bar_wait(empty0 + 8 * slot, (round - 1) & 1u)) {
+                ok = false;
+                break;
+              }
+              // (keys behind the last page are left as they are: their sums are not used)
+              const bool in = lane < boxes && pos < run.end;
+              const int n = __popc(__ballot_sync(0xFFFFFFFFu, in));
+              if (lane == 0) bar_expect(full0 + 8 * slot, uint32_t(n * panels) * box_bytes);
+              __syncwarp();
+              if (in) {   // a page outside the cache is outside the map: zeros
+                const uint32_t dst = ring0 + slot * stage_bytes + uint32_t(lane) * box_bytes;
+                for (int i = 0; i < panels; ++i)
+                  tma_load(dst + uint32_t(i) * kPanel, &p.key_map, full0 + 8 * slot, i * (kByte ? 128 : 64), at.place,
+                           at.page);
+              }
+              __syncwarp();
+              ++issued;
+            }
+          }
+        }
+        // after a wait that gave up: no copy stays in flight
+        for (uint32_t i = !ok && issued > uint32_t(p.ring) ? issued - uint32_t(p.ring) : 0u; !ok && i < issued; ++i)
+          bar_wait(full0 + 8 * (i % uint32_t(p.ring)), (i / uint32_t(p.ring)) & 1u);
+      }
+    } else {
+      const int per_row = p.row_bytes / 16;   // 16-byte pieces of a key
+      for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
+        const Item it = load_item(p, item, per_item);
+        bool queries = false;   // loaded for this item
+        for (int a = 0; a < it.count && ok;) {
+          const Run run = load_run(p, it, a);
+          a = run.b;
+          const int32_t* table = p.table + int64_t(run.seq < 0 ? 0 : run.seq) * p.table_stride;
+          // each lane looks up two keys of a tile, a tile ahead of their use
+          const int32_t mine = it.tile0 * kTile + pw * kProdKeys + lane;
+          KeyPage next0 = fetch_page(p, table, mine, run.tiles > 0 ? run.end : 0);
+          KeyPage next1 = fetch_page(p, table, mine + 32, run.tiles > 0 ? run.end : 0);
+          for (int32_t k = 0; k < run.tiles; ++k) {
+            const KeyPage at0 = next0, at1 = next1;
+            const int32_t end = k + 1 < run.tiles ? run.end : 0;
+            next0 = fetch_page(p, table, mine + (k + 1) * kTile, end);
+            next1 = fetch_page(p, table, mine + (k + 1) * kTile + 32, end);
+            if (!queries) {
+              queries = true;
+              if (!load_queries(it)) {
                 ok = false;
                 break;
               }
             }
-            const uint32_t qb = q0 + buf * q_bytes;
-            const int rows = p.col_tiles * kCols;
-            for (int i = tid; i < rows * per_row; i += kProdThreads) {
-              const int r = i / per_row, piece = i - r * per_row;
-              const int qi = r / kHeads, h = r % kHeads;
-              const bool in = qi < it.count && h < p.heads;
-              const uint8_t* src = p.q;
-              if (in) src += int64_t(it.token0 + qi) * p.q_token_bytes + int64_t(h) * p.q_head_bytes + piece * 16;
-              const int ct = r / kCols, rr = r % kCols;
-              const uint32_t dst = qb + uint32_t(ct * panels + (piece >> 3)) * q_panel + uint32_t(rr) * 128u +
-                                   (uint32_t((piece & 7) ^ (rr & 7)) << 4);
-              copy16(dst, src, in);
+            const uint32_t slot = issued % uint32_t(p.ring), round = issued / uint32_t(p.ring);
+            if (round > 0 && !bar_wait(empty0 + 8 * slot, (round - 1) & 1u)) {
+              ok = false;
+              break;
             }
-            queries = true;
-            ++n_item;
-          }
-          const uint32_t slot = issued % uint32_t(p.ring), round = issued / uint32_t(p.ring);
-          if (round > 0 && !bar_wait(empty0 + 8 * slot, (round - 1) & 1u)) {
-            ok = false;
-            break;
-          }
-          const int64_t off = at.page >= 0 && at.page < p.pages
-                                  ? int64_t(at.page) * p.page_bytes + int64_t(at.place) * p.key_bytes
-                                  : -1;
-          const uint32_t dst0 = ring0 + slot * stage_bytes + uint32_t(pw) * (32 * 128);
-          // each warp brings its own 32 keys, consecutive lanes consecutive pieces
-          if (per_shift >= 0) {
-            const int piece = lane & (per_row - 1), rows = 32 >> per_shift;
-            const uint32_t to = dst0 + uint32_t(piece >> 3) * kPanel;
-            const uint8_t* from = p.keys + piece * 16;
-#pragma unroll 4
-            for (int r = lane >> per_shift; r < 32; r += rows) {
-              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
-              copy16(to + uint32_t(r) * 128u + (uint32_t((piece ^ r) & 7) << 4), from + (o < 0 ? 0 : o), o >= 0);
-            }
-          } else {
-            for (int i = lane; i < 32 * per_row; i += 32) {
+            const int64_t off0 = at0.page >= 0 && at0.page < p.pages
+                                     ? int64_t(at0.page) * p.page_bytes + int64_t(at0.place) * p.key_bytes
+                                     : -1;
+            const int64_t off1 = at1.page >= 0 && at1.page < p.pages
+                                     ? int64_t(at1.page) * p.page_bytes + int64_t(at1.place) * p.key_bytes
+                                     : -1;
+            const uint32_t dst0 = ring0 + slot * stage_bytes + uint32_t(pw) * (kProdKeys * 128);
+            // consecutive lanes bring consecutive pieces
+            for (int i = lane; i < kProdKeys * per_row; i += 32) {
               const int r = i / per_row, piece = i - r * per_row;
-              const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+              const int64_t o0 = __shfl_sync(0xFFFFFFFFu, off0, r & 31), o1 = __shfl_sync(0xFFFFFFFFu, off1, r & 31);
+              const int64_t o = r < 32 ? o0 : o1;
               copy16(dst0 + uint32_t(piece >> 3) * kPanel + uint32_t(r) * 128u + (uint32_t((piece ^ r) & 7) << 4),
                      p.keys + (o < 0 ? 0 : o + piece * 16), o >= 0);
             }
-          }
-          copy_commit();
-          ++issued;
-          if (int32_t(issued - told) > p.lag) {
-            if (p.lag >= 4)
-              copy_wait<4>();
-            else if (p.lag == 3)
-              copy_wait<3>();
-            else if (p.lag == 2)
-              copy_wait<2>();
-            else
-              copy_wait<1>();
-            tell();
+            copy_commit();
+            ++issued;
+            if (int32_t(issued - told) > p.lag) {
+              if (p.lag >= 4)
+                copy_wait<4>();
+              else if (p.lag == 3)
+                copy_wait<3>();
+              else if (p.lag == 2)
+                copy_wait<2>();
+              else
+                copy_wait<1>();
+              tell();
+            }
           }
         }
       }
+      flush();   // also on the way out after a wait that gave up: no copy stays in flight
     }
-    flush();   // also on the way out after a wait that gave up: no copy stays in flight
   } else {
     // ---------------- products ----------------
     uint32_t taken = 0;          // key tiles
@@ -523,6 +598,10 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
         const Run run = load_run(p, it, a);
         a = run.b;
         for (int32_t k = 0; k < run.tiles && ok; ++k) {
+          if (!any && !bar_wait(qfull0 + 8 * (n_item % uint32_t(p.q_bufs)), (n_item / uint32_t(p.q_bufs)) & 1u)) {
+            ok = false;
+            break;
+          }
           any = true;
           const uint32_t slot = taken % uint32_t(p.ring);
           if (!bar_wait(full0 + 8 * slot, (taken / uint32_t(p.ring)) & 1u)) {
@@ -572,10 +651,42 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
   }
 }
 
-template <bool kByte, int kHeads, int kCols>
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The map of a [planes][rows][dim] tensor with boxes of `box_planes` x `box_rows` x `inner` elements.
+bool encode(CUtensorMap* map, int dtype, const void* base, int64_t dim, int64_t rows, int64_t planes, int64_t row_bytes,
+            int64_t plane_bytes, int inner, int box_rows, int box_planes) {
+  static std::atomic<EncodeFn> known;
+  EncodeFn fn = known.load(std::memory_order_relaxed);
+  if (fn == nullptr) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess || f == nullptr) {
+      cudaGetLastError();
+      return false;
+    }
+    fn = reinterpret_cast<EncodeFn>(f);
+    known.store(fn, std::memory_order_relaxed);
+  }
+  const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(rows), cuuint64_t(planes)};
+  const cuuint64_t strides[2] = {cuuint64_t(row_bytes), cuuint64_t(plane_bytes)};
+  const cuuint32_t box[3] = {cuuint32_t(inner), cuuint32_t(box_rows), cuuint32_t(box_planes)};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUtensorMapDataType type = dtype == DSEL_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : dtype == DSEL_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kByte, int kHeads, int kCols, bool kFull>
 int launch_score(const ScoreParams& p, int dtype, int grid, int smem, int dev, cudaStream_t st) {
   static std::atomic<uint64_t> allowed;
-  auto kern = score_kernel<kByte, kHeads, kCols>;
+  auto kern = score_kernel<kByte, kHeads, kCols, kFull>;
   if (allow_smem(reinterpret_cast<const void*>(kern), kScoreSmem, dev, &allowed) != cudaSuccess) return DSEL_ERR_CUDA;
   // D f32, A and B of the operands' type (f16 0, bf16 1; e4m3 0), both K-major, N / 8, M / 16
   const uint32_t type = dtype == DSEL_BF16 ? 1u : 0u;
@@ -594,19 +705,23 @@ int launch_score(const ScoreParams& p, int dtype, int grid, int smem, int dev, c
   return cudaLaunchKernelEx(&cfg, kern, p, idesc) == cudaSuccess ? DSEL_OK : DSEL_ERR_CUDA;
 }
 
+template <bool kByte, int kHeads>
+int launch_heads(const ScoreParams& p, int dtype, bool wide, int grid, int smem, int dev, cudaStream_t st) {
+  if (p.heads == kHeads)
+    return wide ? launch_score<kByte, kHeads, 256, true>(p, dtype, grid, smem, dev, st)
+                : launch_score<kByte, kHeads, kHeads, true>(p, dtype, grid, smem, dev, st);
+  return wide ? launch_score<kByte, kHeads, 256, false>(p, dtype, grid, smem, dev, st)
+              : launch_score<kByte, kHeads, kHeads, false>(p, dtype, grid, smem, dev, st);
+}
+
 template <bool kByte>
-int launch_heads(const ScoreParams& p, int dtype, int hp, bool wide, int grid, int smem, int dev, cudaStream_t st) {
-  if (hp == 16)
-    return wide ? launch_score<kByte, 16, 256>(p, dtype, grid, smem, dev, st)
-                : launch_score<kByte, 16, 16>(p, dtype, grid, smem, dev, st);
-  if (hp == 32)
-    return wide ? launch_score<kByte, 32, 256>(p, dtype, grid, smem, dev, st)
-                : launch_score<kByte, 32, 32>(p, dtype, grid, smem, dev, st);
-  if (hp == 64)
-    return wide ? launch_score<kByte, 64, 256>(p, dtype, grid, smem, dev, st)
-                : launch_score<kByte, 64, 64>(p, dtype, grid, smem, dev, st);
-  return wide ? launch_score<kByte, 128, 256>(p, dtype, grid, smem, dev, st)
-              : launch_score<kByte, 128, 128>(p, dtype, grid, smem, dev, st);
+int launch_type(const ScoreParams& p, int dtype, int hp, bool wide, int grid, int smem, int dev, cudaStream_t st) {
+  switch (hp) {
+    case 16: return launch_heads<kByte, 16>(p, dtype, wide, grid, smem, dev, st);
+    case 32: return launch_heads<kByte, 32>(p, dtype, wide, grid, smem, dev, st);
+    case 64: return launch_heads<kByte, 64>(p, dtype, wide, grid, smem, dev, st);
+    default: return launch_heads<kByte, 128>(p, dtype, wide, grid, smem, dev, st);
+  }
 }
 
 }  // namespace
@@ -638,7 +753,7 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
   if (pages < 0 || page_size < 1 || seqs < 0 || table_width < 0) return DSEL_ERR_SHAPE;
   if (seq_ids == nullptr && seqs != 1 && int64_t(seqs) != tokens) return DSEL_ERR_SHAPE;
   if (row_stride < 1 || row_stride % kStrideReq != 0 || row_stride > INT32_MAX - 64 * kTile) return DSEL_ERR_STRIDE;
-  if (q_head_stride < dim || q_token_stride < 0 || weights_stride < heads || key_stride < dim || page_stride < 0 ||
+  if (q_head_stride < dim || (tokens > 1 && q_token_stride < dim) || weights_stride < heads || key_stride < dim || page_stride < 0 ||
       table_stride < table_width || scale_page_stride < 0)
     return DSEL_ERR_STRIDE;
   // rows of operands are copied in 16-byte pieces
@@ -654,9 +769,6 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
   if (const int st = current_device(&dev, &sms); st != DSEL_OK) return st;
 
   ScoreParams p = {};
-  p.q = static_cast<const uint8_t*>(q);
-  p.q_token_bytes = q_token_stride * eb;
-  p.q_head_bytes = q_head_stride * eb;
   p.weights = weights;
   p.weights_stride = weights_stride;
   p.keys = static_cast<const uint8_t*>(keys);
@@ -693,12 +805,22 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
   p.col_tiles = wide && per_seq > 256 / hp ? 2 : 1;
   const int stage = (p.row_bytes + 127) / 128 * kPanel;
   const int qbytes = p.col_tiles * ((p.row_bytes + 127) / 128) * cols * 128;
-  const int room = kScoreSmem - kBarBytes - 2 * cols * 4;
+  const int room = kScoreSmem - kBarBytes;
   p.q_bufs = (room - 2 * qbytes) / stage >= 4 ? 2 : 1;
   p.ring = (room - p.q_bufs * qbytes) / stage;
   if (p.ring > kMaxRing) p.ring = kMaxRing;
   p.lag = p.ring - 2 > 4 ? 4 : p.ring - 2;
-  const int smem = p.ring * stage + p.q_bufs * qbytes + 2 * cols * 4 + kBarBytes;
+  const int smem = p.ring * stage + p.q_bufs * qbytes + kBarBytes;
+
+  // Queries come as boxes of one accumulator; keys as boxes of a page where the pages fit tiles.
+  const int inner = 128 / eb;   // elements of 128 bytes
+  const int64_t q_head = heads > 1 ? q_head_stride * eb : p.row_bytes;
+  const int64_t q_token = tokens > 1 ? q_token_stride * eb : heads * q_head;
+  if (!encode(&p.q_map, dtype, q, dim, heads, tokens, q_head, q_token, inner, hp, cols / hp)) return DSEL_ERR_STRIDE;
+  p.box_keys = p.page_shift >= 3 && pages > 0 ? (page_size < kTile ? page_size : kTile) : 0;
+  if (p.box_keys > 0 && !encode(&p.key_map, dtype, keys, dim, page_size, pages, p.key_bytes,
+                                pages > 1 ? p.page_bytes : int64_t(page_size) * p.key_bytes, inner, p.box_keys, 1))
+    p.box_keys = 0;
 
   // Key tiles per work item: the count whose items fill whole rounds of the SMs best, an item's own
   // cost (its queries) counted as one tile of a narrow accumulator, two of a wide one.
@@ -721,6 +843,6 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
   p.items = int32_t(groups * p.chunks);
   const int grid = p.items < sms ? p.items : sms;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  return dtype == DSEL_E4M3 ? launch_heads<true>(p, dtype, hp, wide, grid, smem, dev, cs)
-                            : launch_heads<false>(p, dtype, hp, wide, grid, smem, dev, cs);
+  return dtype == DSEL_E4M3 ? launch_type<true>(p, dtype, hp, wide, grid, smem, dev, cs)
+                            : launch_type<false>(p, dtype, hp, wide, grid, smem, dev, cs);
 }
