@@ -127,6 +127,17 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+// True in one lane of a converged warp, the same one every time (a form from which the compiler sees that
+// what follows runs once: the tensor instructions take uniform registers).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0u;
+}
 // Shared-memory descriptor of a K-major operand in 128-byte-swizzled panels: address,
 // 1024 bytes between groups of 8 rows, descriptor version 1, swizzle mode 2 (128 bytes).
 __device__ __forceinline__ uint64_t operand(uint32_t addr) {
@@ -212,23 +223,40 @@ struct Item {
   int32_t tile0;           // first key tile
 };
 
-__device__ __forceinline__ Item load_item(const ScoreParams& p, int32_t item, int per_item) {
+// A place in a ring of `size` and how often the ring went round (its parity); no division on the way.
+struct Cursor {
+  uint32_t at, rounds;
+  __device__ __forceinline__ void step(uint32_t size) {
+    if (++at == size) {
+      at = 0;
+      ++rounds;
+    }
+  }
+};
+
+// What the queries of an item come with, read an item ahead of its use.
+struct ItemRead {
+  int32_t seq, end;
+};
+__device__ __forceinline__ ItemRead read_item(const ScoreParams& p, int32_t item, int per_item) {
+  ItemRead r = {-1, 0};
+  const int lane = int(threadIdx.x & 31);
+  const int64_t t = int64_t(item / p.chunks) * per_item + lane;
+  if (item < p.items && lane < per_item && t < p.tokens) {
+    r.seq = p.seq_mode == 0 ? p.seq_ids[t] : (p.seq_mode == 1 ? int32_t(t) : 0);
+    r.end = p.end[t];
+  }
+  return r;
+}
+__device__ __forceinline__ Item make_item(const ScoreParams& p, int32_t item, int per_item, const ItemRead& r) {
   Item it;
   const int lane = int(threadIdx.x & 31);
   const int32_t group = item / p.chunks;
   it.tile0 = (item - group * p.chunks) * p.chunk;
   it.token0 = group * per_item;
   it.count = p.tokens - it.token0 < per_item ? p.tokens - it.token0 : per_item;
-  const int32_t t = it.token0 + lane;
-  it.seq = -1;
-  it.end = 0;
-  if (lane < it.count) {
-    it.seq = p.seq_mode == 0 ? p.seq_ids[t] : (p.seq_mode == 1 ? t : 0);
-    if (it.seq < 0 || it.seq >= p.seqs) it.seq = -1;
-    it.end = p.end[t];
-    it.end = it.end < 0 ? 0 : (it.end > p.row_stride ? int32_t(p.row_stride) : it.end);
-    if (it.seq < 0) it.end = 0;
-  }
+  it.seq = r.seq < 0 || r.seq >= p.seqs ? -1 : r.seq;
+  it.end = r.end < 0 || it.seq < 0 ? 0 : (r.end > p.row_stride ? int32_t(p.row_stride) : r.end);
   const int32_t before = __shfl_up_sync(0xFFFFFFFFu, it.seq, 1);
   it.starts = __ballot_sync(0xFFFFFFFFu, lane < it.count && (lane == 0 || before != it.seq));
   return it;
@@ -300,7 +328,7 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(done0 + 8 * i, 1);
-      bar_init(free0 + 8 * i, 128);
+      bar_init(free0 + 8 * i, kPerTile > 1 ? 256 : 128);   // warpgroups that read an accumulator
       bar_init(qfull0 + 8 * i, 1);
       bar_init(qfree0 + 8 * i, 1);
     }
@@ -322,103 +350,125 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
 
   if (warp < kEpiWarps) {
     // ---------------- sum over heads, stores ----------------
-    const int b = warp >> 2;                       // warpgroup and accumulator
+    // One query an accumulator: warpgroup b takes accumulator b (every other tile).  Several: both
+    // warpgroups take each accumulator, half of its queries each, while the other one is filled.
+    constexpr bool kShare = kPerTile > 1;
+    constexpr int kMine = kShare ? kPerTile / 2 : 1;       // queries of an accumulator that this warpgroup sums
+    constexpr int kMyCols = kMine * kHeads;
+    constexpr int kAccs = kShare ? 2 : 1;                  // accumulators with queries of their own
+    constexpr int kChunk = kMyCols < 64 ? kMyCols : 64;    // columns read at a time: one query's heads, or several's
+    constexpr int kGroups = kChunk / 8;
+    constexpr int kPerQuery = kHeads < kChunk ? kHeads : kChunk;
+    const int b = warp >> 2;                       // warpgroup
     const int row = (warp & 3) * 32 + (lane >> 2) + (lane & 3) * 8;   // the key of a tile whose sum ends up here
-    const uint32_t acc = tmem + uint32_t(b * kCols) + (uint32_t(warp & 3) << 21);   // lane quarter in bits 16..
-    uint32_t uses = 0;    // times this accumulator was filled
+    const uint32_t acc0 = tmem + (uint32_t(warp & 3) << 21);          // lane quarter in bits 16..
+    uint32_t parity = 0;  // bit a: accumulator a's next fill
     uint32_t turn = 0;    // key tiles so far (col_tiles == 1: accumulators take turns)
     bool ok = true;
+    ItemRead ahead = read_item(p, int32_t(blockIdx.x), per_item);
     for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
-      const Item it = load_item(p, item, per_item);
-      const int first = p.col_tiles == 2 ? b * kPerTile : 0;   // the queries of this warpgroup's columns
+      const Item it = make_item(p, item, per_item, ahead);
+      ahead = read_item(p, item + int32_t(gridDim.x), per_item);
       // the weights of this thread's columns
-      float w[kCols / 4];
+      float w[kAccs][kMyCols / 4];
 #pragma unroll
-      for (int i = 0; i < kCols / 4; ++i) {
-        const int col = (i >> 1) * 8 + (lane & 3) * 2 + (i & 1);
-        const int qi = first + col / kHeads, h = col % kHeads;
-        w[i] = qi < it.count && h < p.heads ? p.weights[int64_t(it.token0 + qi) * p.weights_stride + h] : 0.f;
-      }
+      for (int n = 0; n < kAccs; ++n)
+#pragma unroll
+        for (int i = 0; i < kMyCols / 4; ++i) {
+          const int col = (i >> 1) * 8 + (lane & 3) * 2 + (i & 1);
+          const int qi = n * kPerTile + (kShare ? b * kMine : 0) + col / kHeads, h = col % kHeads;
+          w[n][i] = qi < it.count && qi < per_item && h < p.heads
+                        ? p.weights[int64_t(it.token0 + qi) * p.weights_stride + h]
+                        : 0.f;
+        }
       const int64_t pos0 = int64_t(it.tile0) * kTile;
       const int64_t pos_end = pos0 + int64_t(p.chunk) * kTile < p.row_stride ? pos0 + int64_t(p.chunk) * kTile : p.row_stride;
       for (int a = 0; a < it.count && ok;) {
         const Run run = load_run(p, it, a);
         a = run.b;
-        // queries of this warpgroup's columns in the run
-        const int lo = run.a > first ? run.a : first;
-        const int hi = run.b < first + kPerTile ? run.b : first + kPerTile;
         const int32_t* table = p.table + int64_t(run.seq < 0 ? 0 : run.seq) * p.table_stride;
         // each key's page is fetched a tile of this warpgroup ahead of its use
-        const int skip = p.col_tiles == 2 ? 1 : 2;
-        int32_t k = p.col_tiles == 2 ? 0 : int32_t((turn & 1u) != uint32_t(b));
+        const int skip = kShare ? 1 : 2;
+        int32_t k = kShare ? 0 : int32_t((turn & 1u) != uint32_t(b));
+        const uint32_t turn0 = turn;
         turn += uint32_t(run.tiles);
-        if (lo >= hi) k = run.tiles;
         KeyPage next = fetch_page(p, table, (it.tile0 + k) * kTile + row, k < run.tiles ? run.end : 0);
-        for (; k < run.tiles; k += skip) {
+        for (; k < run.tiles && ok; k += skip) {
           const int32_t pos = (it.tile0 + k) * kTile + row;
           const KeyPage at = next;
           next = fetch_page(p, table, pos + skip * kTile, k + skip < run.tiles ? run.end : 0);
           const bool live = at.page >= 0 && at.page < p.pages;
           float scale = 1.f;
           if (p.key_scale != nullptr && live) scale = p.key_scale[int64_t(at.page) * p.scale_page_stride + at.place];
-          if (!bar_wait(done0 + 8 * b, uses & 1u)) {
-            ok = false;
-            break;
-          }
-          ++uses;
-          tc_fence_after();
-          // up to 64 columns at a time (one query's heads, or those of several) of all 32 keys
-          constexpr int kChunk = kCols < 64 ? kCols : 64;
-          constexpr int kGroups = kChunk / 8;
-          constexpr int kPerQuery = kHeads < kChunk ? kHeads : kChunk;
-          const int c_lo = (lo - first) * kHeads / kChunk, c_hi = ((hi - first) * kHeads + kChunk - 1) / kChunk;
-          float2 s[4];   // sums of keys lane / 4 + 8 j, even and odd columns
 #pragma unroll
-          for (int c = 0; c < kCols / kChunk; ++c) {
-            if (c < c_lo || c >= c_hi) continue;
-            uint32_t x[2][4 * kGroups];
-            tmem_load<kGroups>(acc + uint32_t(c * kChunk), x[0]);
-            tmem_load<kGroups>(acc + (16u << 16) + uint32_t(c * kChunk), x[1]);
-            tmem_wait<kGroups>(x[0]);
-            tmem_wait<kGroups>(x[1]);
-            if (c == c_hi - 1) {   // nothing of the accumulator is left to read
-              tc_fence_before();
-              bar_arrive(free0 + 8 * b);
+          for (int n = 0; n < kAccs; ++n) {
+            // the accumulator's queries in the run, and this warpgroup's of them
+            if (n >= p.col_tiles || run.b <= n * kPerTile || run.a >= (n + 1) * kPerTile) continue;
+            const int first = n * kPerTile + (kShare ? b * kMine : 0);
+            const int lo = run.a > first ? run.a : first;
+            const int hi = run.b < first + kMine ? run.b : first + kMine;
+            const uint32_t acc_i = !kShare ? uint32_t(b) : p.col_tiles == 2 ? uint32_t(n) : (turn0 + uint32_t(k)) & 1u;
+            if (!bar_wait(done0 + 8 * acc_i, (parity >> acc_i) & 1u)) {
+              ok = false;
+              break;
             }
+            parity ^= 1u << acc_i;
+            tc_fence_after();
+            if (lo >= hi) {   // only the other warpgroup has queries here
+              tc_fence_before();
+              bar_arrive(free0 + 8 * acc_i);
+              continue;
+            }
+            const uint32_t acc = acc0 + acc_i * uint32_t(kCols) + uint32_t(kShare ? b * kMyCols : 0);
+            const int c_lo = (lo - first) * kHeads / kChunk, c_hi = ((hi - first) * kHeads + kChunk - 1) / kChunk;
+            float2 s[4];   // sums of keys lane / 4 + 8 j, even and odd columns
 #pragma unroll
-            for (int q = 0; q < kChunk / kPerQuery; ++q) {
-              if (c * kChunk % kHeads == 0) s[0] = s[1] = s[2] = s[3] = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int j = q * kPerQuery / 8; j < (q + 1) * kPerQuery / 8; ++j) {
-                const float2 wj = make_float2(w[(c * kGroups + j) * 2], w[(c * kGroups + j) * 2 + 1]);
-#pragma unroll
-                for (int k4 = 0; k4 < 4; ++k4) {
-                  const uint32_t* xe = &x[k4 >> 1][4 * j + 2 * (k4 & 1)];
-                  float2 y = make_float2(relu(xe[0]), relu(xe[1]));
-                  if (!kFull) {   // columns behind the last head count for nothing, whatever they hold
-                    const int h = (c * kChunk + j * 8) % kHeads + (lane & 3) * 2;
-                    if (h >= p.heads) y.x = 0.f;
-                    if (h + 1 >= p.heads) y.y = 0.f;
-                  }
-                  s[k4] = fma2(y, wj, s[k4]);
-                }
+            for (int c = 0; c < kMyCols / kChunk; ++c) {
+              if (c < c_lo || c >= c_hi) continue;
+              uint32_t x[2][4 * kGroups];
+              tmem_load<kGroups>(acc + uint32_t(c * kChunk), x[0]);
+              tmem_load<kGroups>(acc + (16u << 16) + uint32_t(c * kChunk), x[1]);
+              tmem_wait<kGroups>(x[0]);
+              tmem_wait<kGroups>(x[1]);
+              if (c == c_hi - 1) {   // nothing of the accumulator is left to read
+                tc_fence_before();
+                bar_arrive(free0 + 8 * acc_i);
               }
-              if (kHeads <= kChunk || (c + 1) * kChunk % kHeads == 0) {   // the query's last columns
-                // four sums in each of four lanes: every lane ends up with one key's
-                const float v0 = s[0].x + s[0].y, v1 = s[1].x + s[1].y, v2 = s[2].x + s[2].y, v3 = s[3].x + s[3].y;
-                const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
-                const float a0 = (odd ? v1 : v0) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
-                const float a1 = (odd ? v3 : v2) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v2 : v3, 1);
-                float v = ((high ? a1 : a0) + __shfl_xor_sync(0xFFFFFFFFu, high ? a0 : a1, 2)) * scale;
-                const int qi = first + (c * kChunk + q * kPerQuery) / kHeads;
-                const int32_t end = __shfl_sync(0xFFFFFFFFu, it.end, qi & 31);
-                if (!live || pos >= end) v = -__int_as_float(0x7F800000);
-                if (qi >= lo && qi < hi && pos < p.row_stride) {
-                  const int64_t o = int64_t(it.token0 + qi) * p.row_stride + pos;
-                  if (p.out_f32)
-                    static_cast<float*>(p.out)[o] = v;
-                  else
-                    static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+  #pragma unroll
+              for (int q = 0; q < kChunk / kPerQuery; ++q) {
+                if (c * kChunk % kHeads == 0) s[0] = s[1] = s[2] = s[3] = make_float2(0.f, 0.f);
+  #pragma unroll
+                for (int j = q * kPerQuery / 8; j < (q + 1) * kPerQuery / 8; ++j) {
+                  const float2 wj = make_float2(w[n][(c * kGroups + j) * 2], w[n][(c * kGroups + j) * 2 + 1]);
+  #pragma unroll
+                  for (int k4 = 0; k4 < 4; ++k4) {
+                    const uint32_t* xe = &x[k4 >> 1][4 * j + 2 * (k4 & 1)];
+                    float2 y = make_float2(relu(xe[0]), relu(xe[1]));
+                    if (!kFull) {   // columns behind the last head count for nothing, whatever they hold
+                      const int h = (c * kChunk + j * 8) % kHeads + (lane & 3) * 2;
+                      if (h >= p.heads) y.x = 0.f;
+                      if (h + 1 >= p.heads) y.y = 0.f;
+                    }
+                    s[k4] = fma2(y, wj, s[k4]);
+                  }
+                }
+                if (kHeads <= kChunk || (c + 1) * kChunk % kHeads == 0) {   // the query's last columns
+                  // four sums in each of four lanes: every lane ends up with one key's
+                  const float v0 = s[0].x + s[0].y, v1 = s[1].x + s[1].y, v2 = s[2].x + s[2].y, v3 = s[3].x + s[3].y;
+                  const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
+                  const float a0 = (odd ? v1 : v0) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+                  const float a1 = (odd ? v3 : v2) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v2 : v3, 1);
+                  float v = ((high ? a1 : a0) + __shfl_xor_sync(0xFFFFFFFFu, high ? a0 : a1, 2)) * scale;
+                  const int qi = first + (c * kChunk + q * kPerQuery) / kHeads;
+                  const int32_t end = __shfl_sync(0xFFFFFFFFu, it.end, qi & 31);
+                  if (!live || pos >= end) v = -__int_as_float(0x7F800000);
+                  if (qi >= lo && qi < hi && pos < p.row_stride) {
+                    const int64_t o = int64_t(it.token0 + qi) * p.row_stride + pos;
+                    if (p.out_f32)
+                      static_cast<float*>(p.out)[o] = v;
+                    else
+                      static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+                  }
                 }
               }
             }
@@ -438,29 +488,31 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
   } else if (warp < kEpiWarps + kProdWarps) {
     // ---------------- key tiles and queries ----------------
     const int pw = warp - kEpiWarps;
-    uint32_t issued = 0, told = 0;   // tiles whose copies were started; copied tiles announced as complete
-    uint32_t n_item = 0;             // items that had a tile
+    const uint32_t ring = uint32_t(p.ring);
+    Cursor tile = {0, 0}, told = {0, 0}, qbuf = {0, 0};   // next tile; next copied tile to announce; next queries
+    int pending = 0;                                      // tiles copied but not yet announced
     bool ok = true;
     auto tell = [&]() {   // announce the oldest copied tile that is not yet: it is complete, and visible to the products
       fence_async_shared();
-      bar_arrive(full0 + 8 * (told % uint32_t(p.ring)));
-      ++told;
+      bar_arrive(full0 + 8 * told.at);
+      told.step(ring);
+      --pending;
     };
     auto flush = [&]() {
       copy_wait<0>();
-      while (told < issued) tell();
+      while (pending > 0) tell();
     };
     // the item's queries, before its first tile
     auto load_queries = [&](const Item& it) {
-      const uint32_t buf = n_item % uint32_t(p.q_bufs), use = n_item / uint32_t(p.q_bufs);
-      ++n_item;
+      const uint32_t buf = qbuf.at, use = qbuf.rounds;
+      qbuf.step(uint32_t(p.q_bufs));
       if (pw != 0) return true;
       if (use > 0) {
         // the products that read this buffer may still wait for tiles not yet announced
         if (p.box_keys == 0 && !__all_sync(0xFFFFFFFFu, bar_try(qfree0 + 8 * buf, (use - 1) & 1u))) flush();
         if (!bar_wait(qfree0 + 8 * buf, (use - 1) & 1u)) return false;
       }
-      if (lane == 0) {
+      if (elect_one()) {
         bar_expect(qfull0 + 8 * buf, q_bytes);
         for (int n = 0; n < p.col_tiles; ++n)
           for (int i = 0; i < panels; ++i)
@@ -472,22 +524,32 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     };
     if (p.box_keys > 0) {
       if (pw == 0) {
-        // lane i brings the tile's page i (or its part of a longer page); pages are looked up a tile ahead
-        const int boxes = kTile / p.box_keys;
+        // lane i brings the tile's page i (or its part of a longer page); 32 pages are looked up at once,
+        // that many ahead of their use
+        const int boxes = kTile / p.box_keys, per_batch = 32 / boxes;
         const uint32_t box_bytes = uint32_t(p.box_keys) * 128u;
+        ItemRead ahead = read_item(p, int32_t(blockIdx.x), per_item);
         for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
-          const Item it = load_item(p, item, per_item);
+          const Item it = make_item(p, item, per_item, ahead);
+          ahead = read_item(p, item + int32_t(gridDim.x), per_item);
           bool queries = false;   // loaded for this item
           for (int a = 0; a < it.count && ok;) {
             const Run run = load_run(p, it, a);
             a = run.b;
             const int32_t* table = p.table + int64_t(run.seq < 0 ? 0 : run.seq) * p.table_stride;
-            const int32_t mine = it.tile0 * kTile + lane * p.box_keys;
-            KeyPage next = fetch_page(p, table, mine, lane < boxes && run.tiles > 0 ? run.end : 0);
+            const int32_t start = it.tile0 * kTile;
+            auto fetch = [&](int32_t k) {   // the pages of tiles k .. k + per_batch - 1
+              return fetch_page(p, table, start + k * kTile + lane * p.box_keys, k < run.tiles ? run.end : 0).page;
+            };
+            int32_t batch = -1, next = fetch(0);
             for (int32_t k = 0; k < run.tiles; ++k) {
-              const KeyPage at = next;
-              const int32_t pos = mine + k * kTile;
-              next = fetch_page(p, table, pos + kTile, lane < boxes && k + 1 < run.tiles ? run.end : 0);
+              const int in_batch = k & (per_batch - 1);
+              if (in_batch == 0) {
+                batch = next;
+                next = fetch(k + per_batch);
+              }
+              const int32_t page = __shfl_sync(0xFFFFFFFFu, batch, (in_batch * boxes + lane) & 31);
+              const int32_t pos = start + k * kTile + lane * p.box_keys;
               if (!queries) {
                 queries = true;
                 if (!load_queries(it)) {
@@ -495,8 +557,8 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                   break;
                 }
               }
-              const uint32_t slot = issued % uint32_t(p.ring), round = issued / uint32_t(p.ring);
-              if (round > 0 && !bar_wait(empty0 + 8 * slot, (round - 1) & 1u)) {
+              const uint32_t slot = tile.at;
+              if (tile.rounds > 0 && !bar_wait(empty0 + 8 * slot, (tile.rounds - 1) & 1u)) {
                 ok = false;
                 break;
               }
@@ -508,22 +570,26 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
               if (in) {   // a page outside the cache is outside the map: zeros
                 const uint32_t dst = ring0 + slot * stage_bytes + uint32_t(lane) * box_bytes;
                 for (int i = 0; i < panels; ++i)
-                  tma_load(dst + uint32_t(i) * kPanel, &p.key_map, full0 + 8 * slot, i * (kByte ? 128 : 64), at.place,
-                           at.page);
+                  tma_load(dst + uint32_t(i) * kPanel, &p.key_map, full0 + 8 * slot, i * (kByte ? 128 : 64),
+                           pos & (p.page_size - 1), page);
               }
               __syncwarp();
-              ++issued;
+              tile.step(ring);
             }
           }
         }
-        // after a wait that gave up: no copy stays in flight
-        for (uint32_t i = !ok && issued > uint32_t(p.ring) ? issued - uint32_t(p.ring) : 0u; !ok && i < issued; ++i)
-          bar_wait(full0 + 8 * (i % uint32_t(p.ring)), (i / uint32_t(p.ring)) & 1u);
+        // after a wait that gave up: no copy stays in flight (the last use of each place)
+        for (uint32_t i = 0; !ok && i < ring; ++i) {
+          const uint32_t uses = tile.rounds + (i < tile.at ? 1u : 0u);
+          if (uses > 0) bar_wait(full0 + 8 * i, (uses - 1) & 1u);
+        }
       }
     } else {
       const int per_row = p.row_bytes / 16;   // 16-byte pieces of a key
+      ItemRead ahead = read_item(p, int32_t(blockIdx.x), per_item);
       for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
-        const Item it = load_item(p, item, per_item);
+        const Item it = make_item(p, item, per_item, ahead);
+        ahead = read_item(p, item + int32_t(gridDim.x), per_item);
         bool queries = false;   // loaded for this item
         for (int a = 0; a < it.count && ok;) {
           const Run run = load_run(p, it, a);
@@ -545,8 +611,8 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                 break;
               }
             }
-            const uint32_t slot = issued % uint32_t(p.ring), round = issued / uint32_t(p.ring);
-            if (round > 0 && !bar_wait(empty0 + 8 * slot, (round - 1) & 1u)) {
+            const uint32_t slot = tile.at;
+            if (tile.rounds > 0 && !bar_wait(empty0 + 8 * slot, (tile.rounds - 1) & 1u)) {
               ok = false;
               break;
             }
@@ -566,8 +632,8 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                      p.keys + (o < 0 ? 0 : o + piece * 16), o >= 0);
             }
             copy_commit();
-            ++issued;
-            if (int32_t(issued - told) > p.lag) {
+            tile.step(ring);
+            if (++pending > p.lag) {
               if (p.lag >= 4)
                 copy_wait<4>();
               else if (p.lag == 3)
@@ -585,61 +651,68 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     }
   } else {
     // ---------------- products ----------------
-    uint32_t taken = 0;          // key tiles
+    Cursor tile = {0, 0}, qbuf = {0, 0};
     uint32_t uses[2] = {0, 0};   // accumulators filled
-    uint32_t n_item = 0;
     uint32_t turn = 0;
     bool ok = true;
     const int steps = p.row_bytes / 32;
+    const uint64_t key_operand = operand(ring0), q_operand = operand(q0);
+    ItemRead ahead = read_item(p, int32_t(blockIdx.x), per_item);
     for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
-      const Item it = load_item(p, item, per_item);
+      const Item it = make_item(p, item, per_item, ahead);
+      ahead = read_item(p, item + int32_t(gridDim.x), per_item);
       bool any = false;
       for (int a = 0; a < it.count && ok;) {
         const Run run = load_run(p, it, a);
         a = run.b;
         for (int32_t k = 0; k < run.tiles && ok; ++k) {
-          if (!any && !bar_wait(qfull0 + 8 * (n_item % uint32_t(p.q_bufs)), (n_item / uint32_t(p.q_bufs)) & 1u)) {
+          if (!any && !bar_wait(qfull0 + 8 * qbuf.at, qbuf.rounds & 1u)) {
             ok = false;
             break;
           }
           any = true;
-          const uint32_t slot = taken % uint32_t(p.ring);
-          if (!bar_wait(full0 + 8 * slot, (taken / uint32_t(p.ring)) & 1u)) {
+          if (!bar_wait(full0 + 8 * tile.at, tile.rounds & 1u)) {
             ok = false;
             break;
           }
-          const uint32_t qb = q0 + (n_item % uint32_t(p.q_bufs)) * q_bytes;
-          for (int n = 0; n < p.col_tiles; ++n) {
-            const int b = p.col_tiles == 2 ? n : int(turn & 1u);
-            if (p.col_tiles == 2 && (run.b <= n * kPerTile || run.a >= (n + 1) * kPerTile)) continue;   // no query of it
-            if (uses[b] > 0 && !bar_wait(free0 + 8 * b, (uses[b] - 1) & 1u)) {
+          // (addresses in descriptors count 16 bytes)
+          const uint64_t keys = key_operand + uint64_t(tile.at * (stage_bytes >> 4));
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            // only accumulators with a query of the run
+            if (n >= p.col_tiles || (p.col_tiles == 2 && (run.b <= n * kPerTile || run.a >= (n + 1) * kPerTile))) continue;
+            const uint32_t b = p.col_tiles == 2 ? uint32_t(n) : turn & 1u;
+            const uint32_t before = b == 0 ? uses[0] : uses[1];
+            if (before > 0 && !bar_wait(free0 + 8 * b, (before - 1) & 1u)) {
               ok = false;
               break;
             }
-            ++uses[b];
+            uses[0] += b == 0 ? 1u : 0u;
+            uses[1] += b == 1 ? 1u : 0u;
             tc_fence_after();
-            if (lane == 0) {   // always the same thread: a commit covers its own products
-              for (int s = 0; s < steps; ++s) {
-                const uint32_t in = uint32_t(s & 3) * 32u;
-                mma<kByte>(tmem + uint32_t(b * kCols),
-                           operand(ring0 + slot * stage_bytes + uint32_t(s >> 2) * kPanel + in),
-                           operand(qb + uint32_t(n * panels + (s >> 2)) * q_panel + in), idesc, s > 0);
-              }
+            if (elect_one()) {   // always the same thread: a commit covers its own products
+              const uint64_t queries = q_operand + uint64_t((qbuf.at * q_bytes + uint32_t(n * panels) * q_panel) >> 4);
+              const uint32_t d = tmem + b * uint32_t(kCols);
+#pragma unroll
+              for (int s = 0; s < 8; ++s)
+                if (s < steps)
+                  mma<kByte>(d, keys + uint64_t((s >> 2) * (kPanel >> 4) + (s & 3) * 2),
+                             queries + uint64_t((s >> 2) * (kCols * 128 >> 4) + (s & 3) * 2), idesc, s > 0);
               tc_commit(done0 + 8 * b);
             }
             __syncwarp();
           }
           if (!ok) break;
-          if (lane == 0) tc_commit(empty0 + 8 * slot);
+          if (elect_one()) tc_commit(empty0 + 8 * tile.at);
           __syncwarp();
-          ++taken;
+          tile.step(uint32_t(p.ring));
           ++turn;
         }
       }
       if (any) {
-        if (ok && lane == 0) tc_commit(qfree0 + 8 * (n_item % uint32_t(p.q_bufs)));
+        if (ok && elect_one()) tc_commit(qfree0 + 8 * qbuf.at);
         __syncwarp();
-        ++n_item;
+        qbuf.step(uint32_t(p.q_bufs));
       }
     }
   }
