@@ -40,10 +40,12 @@ constexpr int kEpiWarps = 8;
 constexpr int kProdWarps = 2;
 constexpr int kProdThreads = kProdWarps * 32;
 constexpr int kProdKeys = kTile / kProdWarps;   // keys of a tile that a copying warp brings
-constexpr int kScThreads = (kEpiWarps + kProdWarps + 1) * 32;
+constexpr int kMmaWarps = 2;
+constexpr int kScThreads = (kEpiWarps + kProdWarps + kMmaWarps) * 32;
+constexpr int kMaxAccs = 8;
 constexpr int kMaxRing = 8;
 constexpr int kScoreSmem = 227 * 1024;   // all of a CTA's shared memory
-constexpr int kBarBytes = 256;          // the barriers and the accumulators' address
+constexpr int kBarBytes = 512;          // the barriers and the accumulators' address
 constexpr uint64_t kWaitLimit = 2000000000ull;   // 2 s
 
 struct ScoreParams {
@@ -187,16 +189,6 @@ template <>
 __device__ __forceinline__ void tmem_wait<4>(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
-template <>
-__device__ __forceinline__ void tmem_load<8>(uint32_t addr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-               : "r"(addr));
-}
-template <>
-__device__ __forceinline__ void tmem_wait<8>(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-}
 __device__ __forceinline__ float relu(uint32_t x) {   // a NaN stays one
   float y;
   asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(__uint_as_float(x)));
@@ -302,6 +294,11 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                                                              const uint32_t idesc) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int kPerTile = kCols / kHeads;   // queries of an accumulator
+  // One query an accumulator: key tiles go round as many as fit, so that products run ahead while the
+  // epilogue starts on a work item; warpgroup and product warp b take every other tile.  Several: two of
+  // 256 columns, and both warpgroups take each, half of its queries each, while the other one is filled.
+  constexpr bool kShare = kPerTile > 1;
+  constexpr int kAccs = kShare ? 2 : (512 / kCols < kMaxAccs ? 512 / kCols : kMaxAccs);
   const uint32_t ring0 = shared_addr(smem);
   const int panels = (p.row_bytes + 127) / 128;
   const uint32_t stage_bytes = uint32_t(panels) * kPanel;
@@ -310,12 +307,12 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
   const uint32_t q_bytes = uint32_t(p.col_tiles * panels) * q_panel;     // one query buffer
   uint8_t* tail = smem + p.ring * stage_bytes + p.q_bufs * q_bytes;
   const uint32_t full0 = shared_addr(tail), empty0 = full0 + 8 * kMaxRing;
-  const uint32_t done0 = full0 + 16 * kMaxRing, free0 = done0 + 16, qfull0 = free0 + 16,
+  const uint32_t done0 = full0 + 16 * kMaxRing, free0 = done0 + 8 * kMaxAccs, qfull0 = free0 + 8 * kMaxAccs,
                  qfree0 = qfull0 + 16;
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
   const int per_item = kPerTile * p.col_tiles;
-  static_assert((2 * kMaxRing + 8) * 8 + 8 <= kBarBytes, "barriers outgrew their reservation");
-  uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(tail + (2 * kMaxRing + 8) * 8);
+  static_assert((2 * kMaxRing + 2 * kMaxAccs + 4) * 8 + 8 <= kBarBytes, "barriers outgrew their reservation");
+  uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(tail + (2 * kMaxRing + 2 * kMaxAccs + 4) * 8);
   if ((ring0 & 1023u) != 0u) {   // the swizzled panels need it; the dynamic window starts aligned when it is alone
     if (threadIdx.x == 0) atomicExch(&g_score_status, DSEL_ERR_ALIGN);
     return;
@@ -326,15 +323,17 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
       bar_init(full0 + 8 * i, p.box_keys > 0 ? 1 : kProdThreads);
       bar_init(empty0 + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAccs; ++i) {
       bar_init(done0 + 8 * i, 1);
-      bar_init(free0 + 8 * i, kPerTile > 1 ? 256 : 128);   // warpgroups that read an accumulator
+      bar_init(free0 + 8 * i, kShare ? 256 : 128);   // the warpgroups that read an accumulator
+    }
+    for (int i = 0; i < 2; ++i) {
       bar_init(qfull0 + 8 * i, 1);
-      bar_init(qfree0 + 8 * i, 1);
+      bar_init(qfree0 + 8 * i, kShare ? 1 : kMmaWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  constexpr uint32_t kTmemCols = 2 * kCols < 32 ? 32 : 2 * kCols;
+  constexpr uint32_t kTmemCols = kAccs * kCols;   // a power of two of at least 32
   if (warp == kEpiWarps + kProdWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_addr(tmem_base_sh)),
                  "r"(kTmemCols)
@@ -350,13 +349,11 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
 
   if (warp < kEpiWarps) {
     // ---------------- sum over heads, stores ----------------
-    // One query an accumulator: warpgroup b takes accumulator b (every other tile).  Several: both
-    // warpgroups take each accumulator, half of its queries each, while the other one is filled.
-    constexpr bool kShare = kPerTile > 1;
     constexpr int kMine = kShare ? kPerTile / 2 : 1;       // queries of an accumulator that this warpgroup sums
     constexpr int kMyCols = kMine * kHeads;
-    constexpr int kAccs = kShare ? 2 : 1;                  // accumulators with queries of their own
-    constexpr int kChunk = kMyCols < 64 ? kMyCols : 64;    // columns read at a time: one query's heads, or several's
+    constexpr int kSets = kShare ? 2 : 1;                  // accumulators with queries of their own (col_tiles)
+    constexpr int kChunk = kMyCols < 32 ? kMyCols : 32;    // columns read at a time, the next while one is summed
+    constexpr int kChunks = kMyCols / kChunk;
     constexpr int kGroups = kChunk / 8;
     constexpr int kPerQuery = kHeads < kChunk ? kHeads : kChunk;
     const int b = warp >> 2;                       // warpgroup
@@ -370,9 +367,9 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
       const Item it = make_item(p, item, per_item, ahead);
       ahead = read_item(p, item + int32_t(gridDim.x), per_item);
       // the weights of this thread's columns
-      float w[kAccs][kMyCols / 4];
+      float w[kSets][kMyCols / 4];
 #pragma unroll
-      for (int n = 0; n < kAccs; ++n)
+      for (int n = 0; n < kSets; ++n)
 #pragma unroll
         for (int i = 0; i < kMyCols / 4; ++i) {
           const int col = (i >> 1) * 8 + (lane & 3) * 2 + (i & 1);
@@ -401,13 +398,13 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
           float scale = 1.f;
           if (p.key_scale != nullptr && live) scale = p.key_scale[int64_t(at.page) * p.scale_page_stride + at.place];
 #pragma unroll
-          for (int n = 0; n < kAccs; ++n) {
+          for (int n = 0; n < kSets; ++n) {
             // the accumulator's queries in the run, and this warpgroup's of them
             if (n >= p.col_tiles || run.b <= n * kPerTile || run.a >= (n + 1) * kPerTile) continue;
             const int first = n * kPerTile + (kShare ? b * kMine : 0);
             const int lo = run.a > first ? run.a : first;
             const int hi = run.b < first + kMine ? run.b : first + kMine;
-            const uint32_t acc_i = !kShare ? uint32_t(b) : p.col_tiles == 2 ? uint32_t(n) : (turn0 + uint32_t(k)) & 1u;
+            const uint32_t acc_i = kShare && p.col_tiles == 2 ? uint32_t(n) : (turn0 + uint32_t(k)) & uint32_t(kAccs - 1);
             if (!bar_wait(done0 + 8 * acc_i, (parity >> acc_i) & 1u)) {
               ok = false;
               break;
@@ -420,29 +417,32 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
               continue;
             }
             const uint32_t acc = acc0 + acc_i * uint32_t(kCols) + uint32_t(kShare ? b * kMyCols : 0);
-            const int c_lo = (lo - first) * kHeads / kChunk, c_hi = ((hi - first) * kHeads + kChunk - 1) / kChunk;
+            uint32_t x[2][2][4 * kGroups];
+            auto read = [&](int c) {
+              tmem_load<kGroups>(acc + uint32_t(c * kChunk), x[c & 1][0]);
+              tmem_load<kGroups>(acc + (16u << 16) + uint32_t(c * kChunk), x[c & 1][1]);
+            };
             float2 s[4];   // sums of keys lane / 4 + 8 j, even and odd columns
+            read(0);
 #pragma unroll
-            for (int c = 0; c < kMyCols / kChunk; ++c) {
-              if (c < c_lo || c >= c_hi) continue;
-              uint32_t x[2][4 * kGroups];
-              tmem_load<kGroups>(acc + uint32_t(c * kChunk), x[0]);
-              tmem_load<kGroups>(acc + (16u << 16) + uint32_t(c * kChunk), x[1]);
-              tmem_wait<kGroups>(x[0]);
-              tmem_wait<kGroups>(x[1]);
-              if (c == c_hi - 1) {   // nothing of the accumulator is left to read
+            for (int c = 0; c < kChunks; ++c) {
+              tmem_wait<kGroups>(x[c & 1][0]);
+              tmem_wait<kGroups>(x[c & 1][1]);
+              if (c + 1 < kChunks) {
+                read(c + 1);
+              } else {   // nothing of the accumulator is left to read
                 tc_fence_before();
                 bar_arrive(free0 + 8 * acc_i);
               }
-  #pragma unroll
+#pragma unroll
               for (int q = 0; q < kChunk / kPerQuery; ++q) {
                 if (c * kChunk % kHeads == 0) s[0] = s[1] = s[2] = s[3] = make_float2(0.f, 0.f);
-  #pragma unroll
+#pragma unroll
                 for (int j = q * kPerQuery / 8; j < (q + 1) * kPerQuery / 8; ++j) {
                   const float2 wj = make_float2(w[n][(c * kGroups + j) * 2], w[n][(c * kGroups + j) * 2 + 1]);
-  #pragma unroll
+#pragma unroll
                   for (int k4 = 0; k4 < 4; ++k4) {
-                    const uint32_t* xe = &x[k4 >> 1][4 * j + 2 * (k4 & 1)];
+                    const uint32_t* xe = &x[c & 1][k4 >> 1][4 * j + 2 * (k4 & 1)];
                     float2 y = make_float2(relu(xe[0]), relu(xe[1]));
                     if (!kFull) {   // columns behind the last head count for nothing, whatever they hold
                       const int h = (c * kChunk + j * 8) % kHeads + (lane & 3) * 2;
@@ -459,6 +459,7 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                   const float a0 = (odd ? v1 : v0) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
                   const float a1 = (odd ? v3 : v2) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v2 : v3, 1);
                   float v = ((high ? a1 : a0) + __shfl_xor_sync(0xFFFFFFFFu, high ? a0 : a1, 2)) * scale;
+                  // (queries of other runs are summed with the others and not stored)
                   const int qi = first + (c * kChunk + q * kPerQuery) / kHeads;
                   const int32_t end = __shfl_sync(0xFFFFFFFFu, it.end, qi & 31);
                   if (!live || pos >= end) v = -__int_as_float(0x7F800000);
@@ -504,14 +505,12 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     };
     // the item's queries, before its first tile
     auto load_queries = [&](const Item& it) {
-      const uint32_t buf = qbuf.at, use = qbuf.rounds;
+      const uint32_t buf = qbuf.at, was = (qbuf.rounds & 1u) ^ 1u;
       qbuf.step(uint32_t(p.q_bufs));
       if (pw != 0) return true;
-      if (use > 0) {
-        // the products that read this buffer may still wait for tiles not yet announced
-        if (p.box_keys == 0 && !__all_sync(0xFFFFFFFFu, bar_try(qfree0 + 8 * buf, (use - 1) & 1u))) flush();
-        if (!bar_wait(qfree0 + 8 * buf, (use - 1) & 1u)) return false;
-      }
+      // the products that read this buffer may still wait for tiles not yet announced
+      if (p.box_keys == 0 && !__all_sync(0xFFFFFFFFu, bar_try(qfree0 + 8 * buf, was))) flush();
+      if (!bar_wait(qfree0 + 8 * buf, was)) return false;
       if (elect_one()) {
         bar_expect(qfull0 + 8 * buf, q_bytes);
         for (int n = 0; n < p.col_tiles; ++n)
@@ -523,9 +522,10 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
       return true;
     };
     if (p.box_keys > 0) {
-      if (pw == 0) {
-        // lane i brings the tile's page i (or its part of a longer page); 32 pages are looked up at once,
-        // that many ahead of their use
+      {
+        // The warps take every other tile.  Lane i brings its page i (or its part of a longer page); 32 pages
+        // are looked up at once, that many ahead of their use.
+        uint32_t turn = 0;
         const int boxes = kTile / p.box_keys, per_batch = 32 / boxes;
         const uint32_t box_bytes = uint32_t(p.box_keys) * 128u;
         ItemRead ahead = read_item(p, int32_t(blockIdx.x), per_item);
@@ -557,23 +557,25 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                   break;
                 }
               }
-              const uint32_t slot = tile.at;
-              if (tile.rounds > 0 && !bar_wait(empty0 + 8 * slot, (tile.rounds - 1) & 1u)) {
-                ok = false;
-                break;
+              if (int(turn++ & 1u) == pw) {
+                const uint32_t slot = tile.at;
+                if (!bar_wait(empty0 + 8 * slot, (tile.rounds & 1u) ^ 1u)) {
+                  ok = false;
+                  break;
+                }
+                // (keys behind the last page are left as they are: their sums are not used)
+                const bool in = lane < boxes && pos < run.end;
+                const int n = __popc(__ballot_sync(0xFFFFFFFFu, in));
+                if (elect_one()) bar_expect(full0 + 8 * slot, uint32_t(n * panels) * box_bytes);
+                __syncwarp();
+                if (in) {   // a page outside the cache is outside the map: zeros
+                  const uint32_t dst = ring0 + slot * stage_bytes + uint32_t(lane) * box_bytes;
+                  for (int i = 0; i < panels; ++i)
+                    tma_load(dst + uint32_t(i) * kPanel, &p.key_map, full0 + 8 * slot, i * (kByte ? 128 : 64),
+                             pos & (p.page_size - 1), page);
+                }
+                __syncwarp();
               }
-              // (keys behind the last page are left as they are: their sums are not used)
-              const bool in = lane < boxes && pos < run.end;
-              const int n = __popc(__ballot_sync(0xFFFFFFFFu, in));
-              if (lane == 0) bar_expect(full0 + 8 * slot, uint32_t(n * panels) * box_bytes);
-              __syncwarp();
-              if (in) {   // a page outside the cache is outside the map: zeros
-                const uint32_t dst = ring0 + slot * stage_bytes + uint32_t(lane) * box_bytes;
-                for (int i = 0; i < panels; ++i)
-                  tma_load(dst + uint32_t(i) * kPanel, &p.key_map, full0 + 8 * slot, i * (kByte ? 128 : 64),
-                           pos & (p.page_size - 1), page);
-              }
-              __syncwarp();
               tile.step(ring);
             }
           }
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
         // after a wait that gave up: no copy stays in flight (the last use of each place)
         for (uint32_t i = 0; !ok && i < ring; ++i) {
           const uint32_t uses = tile.rounds + (i < tile.at ? 1u : 0u);
-          if (uses > 0) bar_wait(full0 + 8 * i, (uses - 1) & 1u);
+          if (uses > 0) bar_wait(full0 + 8 * i, (uses - 1) & 1u);   // (or the other warp's, given up on as well)
         }
       }
     } else {
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
               }
             }
             const uint32_t slot = tile.at;
-            if (tile.rounds > 0 && !bar_wait(empty0 + 8 * slot, (tile.rounds - 1) & 1u)) {
+            if (!bar_wait(empty0 + 8 * slot, (tile.rounds & 1u) ^ 1u)) {
               ok = false;
               break;
             }
@@ -652,9 +654,10 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
   } else {
     // ---------------- products ----------------
     Cursor tile = {0, 0}, qbuf = {0, 0};
-    uint32_t uses[2] = {0, 0};   // accumulators filled
-    uint32_t turn = 0;
-    bool ok = true;
+    const int mw = warp - kEpiWarps - kProdWarps;
+    uint32_t parity = 0;   // bit a: accumulator a's next fill
+    uint32_t turn = 0;     // key tiles so far
+    bool ok = mw == 0 || !kShare;
     const int steps = p.row_bytes / 32;
     const uint64_t key_operand = operand(ring0), q_operand = operand(q0);
     ItemRead ahead = read_item(p, int32_t(blockIdx.x), per_item);
@@ -671,6 +674,12 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
             break;
           }
           any = true;
+          if (!kShare && int(turn & 1u) != mw) {   // the other warp's
+            parity ^= 1u << (turn & uint32_t(kAccs - 1));
+            tile.step(uint32_t(p.ring));
+            ++turn;
+            continue;
+          }
           if (!bar_wait(full0 + 8 * tile.at, tile.rounds & 1u)) {
             ok = false;
             break;
@@ -678,17 +687,15 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
           // (addresses in descriptors count 16 bytes)
           const uint64_t keys = key_operand + uint64_t(tile.at * (stage_bytes >> 4));
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < (kShare ? 2 : 1); ++n) {
             // only accumulators with a query of the run
-            if (n >= p.col_tiles || (p.col_tiles == 2 && (run.b <= n * kPerTile || run.a >= (n + 1) * kPerTile))) continue;
-            const uint32_t b = p.col_tiles == 2 ? uint32_t(n) : turn & 1u;
-            const uint32_t before = b == 0 ? uses[0] : uses[1];
-            if (before > 0 && !bar_wait(free0 + 8 * b, (before - 1) & 1u)) {
+            if (n >= p.col_tiles || run.b <= n * kPerTile || run.a >= (n + 1) * kPerTile) continue;
+            const uint32_t b = kShare && p.col_tiles == 2 ? uint32_t(n) : turn & uint32_t(kAccs - 1);
+            if (!bar_wait(free0 + 8 * b, ((parity >> b) & 1u) ^ 1u)) {
               ok = false;
               break;
             }
-            uses[0] += b == 0 ? 1u : 0u;
-            uses[1] += b == 1 ? 1u : 0u;
+            parity ^= 1u << b;
             tc_fence_after();
             if (elect_one()) {   // always the same thread: a commit covers its own products
               const uint64_t queries = q_operand + uint64_t((qbuf.at * q_bytes + uint32_t(n * panels) * q_panel) >> 4);
