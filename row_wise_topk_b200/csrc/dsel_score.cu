@@ -215,6 +215,17 @@ struct Item {
   int32_t tile0;           // first key tile
 };
 
+// Stores y as float32 or bfloat16 where `on`, without a branch: the code around it stays one block.
+__device__ __forceinline__ void store_if(bool on, bool f32, uint64_t at, float y) {
+  const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b16 h;\n\t"
+      "setp.ne.u32 p, %0, 0;\n\tsetp.ne.u32 q, %1, 0;\n\tcvt.u16.u32 h, %4;\n\t"
+      "@p st.global.b16 [%2], h;\n\t@q st.global.f32 [%2], %3;\n\t}" ::"r"(uint32_t(on && !f32)),
+      "r"(uint32_t(on && f32)), "l"(at), "f"(y), "r"(h)
+      : "memory");
+}
+
 // A place in a ring of `size` and how often the ring went round (its parity); no division on the way.
 struct Cursor {
   uint32_t at, rounds;
@@ -378,6 +389,32 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                         ? p.weights[int64_t(it.token0 + qi) * p.weights_stride + h]
                         : 0.f;
         }
+      // Queries that were summed, four sums in each of four lanes: finish() leaves one key's in every lane
+      // and stores it.  It runs beside the next sum, whose arithmetic fills its waits.
+      struct {
+        float s[kChunk / kPerQuery][4];
+        int32_t pos, q, lo, hi;   // stored: queries q.. in [lo, hi)
+        uint64_t at;              // address of query 0's score of this key
+        float scale;
+        bool live;
+      } last = {};
+      const bool out_f32 = p.out_f32 != 0;
+      auto finish = [&]() {
+#pragma unroll
+        for (int i = 0; i < kChunk / kPerQuery; ++i) {
+          const float* v = last.s[i];
+          const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
+          const float a0 = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[1], 1);
+          const float a1 = (odd ? v[3] : v[2]) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v[2] : v[3], 1);
+          float y = ((high ? a1 : a0) + __shfl_xor_sync(0xFFFFFFFFu, high ? a0 : a1, 2)) * last.scale;
+          const int qi = last.q + i;
+          const int32_t end = __shfl_sync(0xFFFFFFFFu, it.end, qi & 31);
+          if (!last.live || last.pos >= end) y = -__int_as_float(0x7F800000);
+          // (queries of other runs are summed with the others and not stored)
+          store_if(qi >= last.lo && qi < last.hi && last.pos < p.row_stride, out_f32,
+                   last.at + ((int64_t(qi) * int32_t(p.row_stride)) << (out_f32 ? 2 : 1)), y);
+        }
+      };
       const int64_t pos0 = int64_t(it.tile0) * kTile;
       const int64_t pos_end = pos0 + int64_t(p.chunk) * kTile < p.row_stride ? pos0 + int64_t(p.chunk) * kTile : p.row_stride;
       for (int a = 0; a < it.count && ok;) {
@@ -434,6 +471,7 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                 tc_fence_before();
                 bar_arrive(free0 + 8 * acc_i);
               }
+              if ((kHeads <= kChunk || c * kChunk % kHeads == 0)) finish();   // its waits pass under this sum
 #pragma unroll
               for (int q = 0; q < kChunk / kPerQuery; ++q) {
                 if (c * kChunk % kHeads == 0) s[0] = s[1] = s[2] = s[3] = make_float2(0.f, 0.f);
@@ -453,28 +491,25 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                   }
                 }
                 if (kHeads <= kChunk || (c + 1) * kChunk % kHeads == 0) {   // the query's last columns
-                  // four sums in each of four lanes: every lane ends up with one key's
-                  const float v0 = s[0].x + s[0].y, v1 = s[1].x + s[1].y, v2 = s[2].x + s[2].y, v3 = s[3].x + s[3].y;
-                  const bool odd = (lane & 1) != 0, high = (lane & 2) != 0;
-                  const float a0 = (odd ? v1 : v0) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
-                  const float a1 = (odd ? v3 : v2) + __shfl_xor_sync(0xFFFFFFFFu, odd ? v2 : v3, 1);
-                  float v = ((high ? a1 : a0) + __shfl_xor_sync(0xFFFFFFFFu, high ? a0 : a1, 2)) * scale;
-                  // (queries of other runs are summed with the others and not stored)
-                  const int qi = first + (c * kChunk + q * kPerQuery) / kHeads;
-                  const int32_t end = __shfl_sync(0xFFFFFFFFu, it.end, qi & 31);
-                  if (!live || pos >= end) v = -__int_as_float(0x7F800000);
-                  if (qi >= lo && qi < hi && pos < p.row_stride) {
-                    const int64_t o = int64_t(it.token0 + qi) * p.row_stride + pos;
-                    if (p.out_f32)
-                      static_cast<float*>(p.out)[o] = v;
-                    else
-                      static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
-                  }
+#pragma unroll
+                  for (int k4 = 0; k4 < 4; ++k4) last.s[q][k4] = s[k4].x + s[k4].y;
                 }
+              }
+              if (kHeads <= kChunk || (c + 1) * kChunk % kHeads == 0) {
+                last.pos = pos;
+                last.q = first + c * kChunk / kHeads;
+                last.lo = lo;
+                last.hi = hi;
+                last.at = reinterpret_cast<uint64_t>(p.out) +
+                          uint64_t((int64_t(it.token0) * p.row_stride + pos) << (out_f32 ? 2 : 1));
+                last.scale = scale;
+                last.live = live;
               }
             }
           }
         }
+        finish();
+        last.hi = 0;
         // -inf behind the run's last tile (both warpgroups' threads, 16 bytes each)
         const int64_t from = pos0 + int64_t(run.tiles) * kTile;
         const int step = p.out_f32 ? 4 : 8;
