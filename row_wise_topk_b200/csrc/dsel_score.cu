@@ -421,19 +421,27 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
         const Run run = load_run(p, it, a);
         a = run.b;
         const int32_t* table = p.table + int64_t(run.seq < 0 ? 0 : run.seq) * p.table_stride;
-        // each key's page is fetched a tile of this warpgroup ahead of its use
+        // Each key's scale is read one tile of this warpgroup ahead of its use, its page two.
         const int skip = kShare ? 1 : 2;
         int32_t k = kShare ? 0 : int32_t((turn & 1u) != uint32_t(b));
         const uint32_t turn0 = turn;
         turn += uint32_t(run.tiles);
-        KeyPage next = fetch_page(p, table, (it.tile0 + k) * kTile + row, k < run.tiles ? run.end : 0);
+        auto page_of = [&](int32_t tile) {
+          return fetch_page(p, table, (it.tile0 + tile) * kTile + row, tile < run.tiles ? run.end : 0);
+        };
+        auto exists = [&](const KeyPage& at) { return at.page >= 0 && at.page < p.pages; };
+        auto scale_of = [&](const KeyPage& at) {
+          return p.key_scale != nullptr && exists(at) ? p.key_scale[int64_t(at.page) * p.scale_page_stride + at.place] : 1.f;
+        };
+        KeyPage at = page_of(k), next = page_of(k + skip);
+        float scale = scale_of(at);
         for (; k < run.tiles && ok; k += skip) {
           const int32_t pos = (it.tile0 + k) * kTile + row;
-          const KeyPage at = next;
-          next = fetch_page(p, table, pos + skip * kTile, k + skip < run.tiles ? run.end : 0);
-          const bool live = at.page >= 0 && at.page < p.pages;
-          float scale = 1.f;
-          if (p.key_scale != nullptr && live) scale = p.key_scale[int64_t(at.page) * p.scale_page_stride + at.place];
+          const bool live = exists(at);
+          const float scale_now = scale;
+          scale = scale_of(next);
+          at = next;
+          next = page_of(k + 2 * skip);
 #pragma unroll
           for (int n = 0; n < kSets; ++n) {
             // the accumulator's queries in the run, and this warpgroup's of them
@@ -502,7 +510,7 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                 last.hi = hi;
                 last.at = reinterpret_cast<uint64_t>(p.out) +
                           uint64_t((int64_t(it.token0) * p.row_stride + pos) << (out_f32 ? 2 : 1));
-                last.scale = scale;
+                last.scale = scale_now;
                 last.live = live;
               }
             }
