@@ -120,6 +120,17 @@ def test_long_rows_many_items():
     check(run(a), a)
 
 
+@pytest.mark.parametrize("page", [16, 20])
+@pytest.mark.parametrize("heads", [8, 64])
+def test_many_short_sequences(page, heads):
+    # several work items for each CTA, rows of zero to six tiles in no order, a scale for each key
+    n = 700
+    ends = [(i * 37) % 730 if i % 5 else (i * 64) % 390 for i in range(n)]
+    a = make(page + heads, seqs=n, tokens=n, heads=heads, dim=32, page=page, width=-(-736 // page), dtype="e4m3", scale=True,
+             ends=ends)
+    check(run(a), a)
+
+
 def test_strides():
     a = make(12, tokens=6, heads=5, dim=64, page=10, width=9, ends=[90, 80, 3, 0, 55, 90], scale=True)
     d = {k: v.cuda() for k, v in a.items()}
