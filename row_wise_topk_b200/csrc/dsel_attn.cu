@@ -30,7 +30,10 @@ namespace {
 
 constexpr int kAtWarps = 4;
 constexpr int kAtThreads = kAtWarps * 32;
-constexpr int kAtTile = 32;        // positions per tile
+// Positions per tile.  A group of one warp owns a whole ring, so its tiles are small enough that eight
+// warps fit an SM (with tiles of 32 four did, and a 1,024-query chunk took 443 us); groups of two and
+// four warps share theirs.
+constexpr int at_tile(int row_warps) { return row_warps == 1 ? 16 : 32; }
 constexpr int kAtMaxStages = 3;
 constexpr int kAtMaxCluster = 8;
 constexpr int kPitchPad = 8;       // floats: rows of the partial sums fall on different banks
@@ -57,6 +60,7 @@ struct AttnParams {
   int32_t kv_heads, group, row_tiles;
   int32_t take, block, block_shift;
   int32_t tiles;        // tiles of the whole list
+  int32_t rows_even;    // places lie row_bytes apart across pages too, in k as in v: one 32-bit place says where
   int32_t stages;
 };
 
@@ -146,20 +150,17 @@ __device__ __forceinline__ int32_t list_position(const AttnParams& p, const void
   return pos < int64_t(end) ? int32_t(pos) : -1;
 }
 
+// The page of a position and its place in it; page < 0: none.
 struct Place {
-  int64_t k, v;   // byte offsets of the rows; k < 0: none
+  int32_t page, row;
 };
 __device__ __forceinline__ Place locate(const AttnParams& p, const int32_t* table, int32_t pos) {
-  Place at = {-1, -1};
+  Place at = {-1, 0};
   if (pos >= 0) {
     const int32_t i = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
-    int32_t page = -1;
-    if (i < p.table_width) page = table[i];
-    if (page >= 0 && page < p.pages) {
-      const int64_t r = pos - i * p.page_size;
-      at.k = int64_t(page) * p.k_page_bytes + r * p.k_row_bytes;
-      at.v = int64_t(page) * p.v_page_bytes + r * p.v_row_bytes;
-    }
+    if (i < p.table_width) at.page = table[i];
+    if (at.page >= p.pages) at.page = -1;
+    at.row = pos - i * p.page_size;
   }
   return at;
 }
@@ -171,6 +172,7 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
   constexpr int kRows = 16 * kRowWarps;                  // query heads of the CTA
   constexpr int kRowBytes = kDim * 2;
   constexpr int kPieces = kRowBytes / 16;
+  constexpr int kAtTile = at_tile(kRowWarps);
   constexpr int kTileBytes = kAtTile * kRowBytes;        // keys of a tile; its values follow
   constexpr int kPitch = kDim + kPitchPad;
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
@@ -221,29 +223,42 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
   const int32_t mine = p.tiles > first ? (p.tiles - first + step - 1) / step : 0;   // tiles of this group
 
   // Two loads lie between a list entry and its rows (the index, the page): each is fetched a tile ahead of its use.
-  int32_t pos_next = mine > 0 ? list_position(p, idx, first * kAtTile + lane, end) : -1;
-  auto issue = [&](int32_t i) {   // starts the copies of the group's tile i
-    if (i < mine) {
-      const Place at = locate(p, table, pos_next);
-      pos_next = i + 1 < mine ? list_position(p, idx, (first + (i + 1) * step) * kAtTile + lane, end) : -1;
-      const uint32_t any = __ballot_sync(0xFFFFFFFFu, at.k >= 0);
-      if (any != 0u) {
-        const uint32_t dst = ring + uint32_t(i % p.stages) * (2 * kTileBytes);
-        constexpr int kPerPass = 32 / kPieces;   // rows per pass of a warp
-        const int piece = lane % kPieces;
+  auto entry = [&](int32_t i) {   // this lane's position in the group's tile i
+    return i < mine && lane < kAtTile ? list_position(p, idx, (first + i * step) * kAtTile + lane, end) : -1;
+  };
+  int32_t pos_next = entry(0);
+  constexpr int kPerPass = 32 / kPieces;   // rows that a warp copies at once
+  const int piece = lane % kPieces;
+  auto issue = [&](int32_t i) -> uint32_t {   // starts the copies of the group's tile i; which of its positions exist
+    if (i >= mine) return 0u;
+    const Place at = locate(p, table, pos_next);
+    pos_next = entry(i + 1);
+    const uint32_t any = __ballot_sync(0xFFFFFFFFu, at.page >= 0);
+    if (any == 0u) return 0u;
+    const uint32_t dst = ring + uint32_t(i % p.stages) * (2 * kTileBytes);
+    if (p.rows_even) {
+      const int32_t slot = at.page >= 0 ? at.page * p.page_size + at.row : -1;
 #pragma unroll
-        for (int r = 0; r < kAtTile / kRowWarps; r += kPerPass) {
-          const int row = rw * (kAtTile / kRowWarps) + r + lane / kPieces;
-          const int64_t ok = __shfl_sync(0xFFFFFFFFu, at.k, row);
-          const int64_t ov = __shfl_sync(0xFFFFFFFFu, at.v, row);
-          const uint32_t to = dst + uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4);
-          copy16(to, kbase + (ok >= 0 ? ok + piece * 16 : 0), ok >= 0);
-          copy16(to + kTileBytes, vbase + (ok >= 0 ? ov + piece * 16 : 0), ok >= 0);
-        }
+      for (int r = 0; r < kAtTile / kRowWarps; r += kPerPass) {
+        const int row = rw * (kAtTile / kRowWarps) + r + lane / kPieces;
+        const int32_t s = __shfl_sync(0xFFFFFFFFu, slot, row);
+        const uint32_t to = dst + uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4);
+        const int64_t o = int64_t(s < 0 ? 0 : s) * int32_t(p.k_row_bytes) + piece * 16;
+        copy16(to, kbase + o, s >= 0);
+        copy16(to + kTileBytes, vbase + o, s >= 0);
       }
-      return any;
+    } else {
+#pragma unroll 2
+      for (int r = 0; r < kAtTile / kRowWarps; r += kPerPass) {
+        const int row = rw * (kAtTile / kRowWarps) + r + lane / kPieces;
+        const int64_t page = __shfl_sync(0xFFFFFFFFu, at.page, row), place = __shfl_sync(0xFFFFFFFFu, at.row, row);
+        const uint32_t to = dst + uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4);
+        const bool in = page >= 0;
+        copy16(to, kbase + (in ? page * p.k_page_bytes + place * p.k_row_bytes + piece * 16 : 0), in);
+        copy16(to + kTileBytes, vbase + (in ? page * p.v_page_bytes + place * p.v_row_bytes + piece * 16 : 0), in);
+      }
     }
-    return 0u;
+    return any;
   };
 
   uint32_t live[kAtMaxStages];   // which positions of the tiles in flight exist
@@ -432,7 +447,8 @@ int launch_attn(AttnParams p, int64_t units, int dev, int sms, cudaStream_t st) 
   static std::atomic<uint64_t> allowed;
   auto kern = attn_kernel<kBf16, kDim, kRowWarps>;
   constexpr int kGroups = kAtWarps / kRowWarps;
-  constexpr int kStageBytes = kGroups * 2 * kAtTile * kDim * 2;
+  constexpr int kStageBytes = kGroups * 2 * at_tile(kRowWarps) * kDim * 2;
+  p.tiles = int32_t((int64_t(p.take) * p.block + at_tile(kRowWarps) - 1) / at_tile(kRowWarps));
   // CTAs per (query, key head): as many as fill the SMs twice, but none without a tile for each of its groups
   int cluster = 1;
   while (cluster < kAtMaxCluster && units * cluster * 2 <= int64_t(sms) * 2 && cluster * 2 * kGroups <= p.tiles) cluster *= 2;
@@ -536,7 +552,9 @@ DSEL_API int dsel_sparse_attn(const void* q, int dtype, int64_t tokens, int32_t 
   p.take = take;
   p.block = block;
   p.block_shift = log2_of(block);
-  p.tiles = int32_t((int64_t(take) * block + kAtTile - 1) / kAtTile);
+  p.rows_even = k_page_stride == page_size * k_row_stride && v_page_stride == k_page_stride &&
+                v_row_stride == k_row_stride && int64_t(pages) * page_size <= INT32_MAX &&
+                k_row_stride * 2 <= INT32_MAX;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (dtype == DSEL_BF16)
     return dim == 64 ? launch_rows<true, 64>(p, tokens, dev, sms, cs) : launch_rows<true, 128>(p, tokens, dev, sms, cs);
