@@ -53,7 +53,9 @@ struct AttnParams {
   const int32_t* end;
   void* out;
   float* lse;
-  float scale_log2;     // scale * log2(e): the softmax runs on powers of two
+  float scale_log2;     // |scale| * log2(e): the softmax runs on powers of two
+  uint32_t q_flip;      // sign bits of a pair of 16-bit values where scale < 0
+  uint32_t q_keep;      // no bits where scale is 0: the products are, and scale_log2 is 1
   int32_t idx_i64;
   int32_t pages, page_size, page_shift;
   int32_t seqs, table_width, seq_mode;
@@ -142,7 +144,15 @@ __device__ __forceinline__ void group_sync(int group) {
 
 // Position in its sequence of entry l of the list, or -1: none, or behind `end`.
 __device__ __forceinline__ int32_t list_position(const AttnParams& p, const void* idx, int32_t l, int32_t end) {
-  const int32_t j = p.block_shift >= 0 ? l >> p.block_shift : l / p.block;
+  if (p.block_shift >= 0 && !p.idx_i64) {   // the plain case in 32 bits: an index that passes the test gives a position
+    const int32_t j = l >> p.block_shift;
+    if (j >= p.take) return -1;
+    const uint32_t i = static_cast<const uint32_t*>(idx)[j];
+    if (end <= 0 || i > uint32_t(end - 1) >> p.block_shift) return -1;
+    const int32_t pos = int32_t(i << p.block_shift) + (l - (j << p.block_shift));
+    return pos < end ? pos : -1;
+  }
+  const int32_t j = l / p.block;
   if (j >= p.take) return -1;
   const int64_t i = p.idx_i64 ? static_cast<const int64_t*>(idx)[j] : int64_t(static_cast<const int32_t*>(idx)[j]);
   if (i < 0 || i > int64_t(end)) return -1;
@@ -195,7 +205,8 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
   const uint8_t* kbase = p.k + int64_t(kvh) * p.k_head_bytes;
   const uint8_t* vbase = p.v + int64_t(kvh) * p.v_head_bytes;
 
-  // this warp's query heads as A fragments
+  // this warp's query heads as A fragments (with a negative scale their negatives: scores then only grow with
+  // the products, and the maximum is that of the products)
   const int row0 = rt * kRows + rw * 16;    // first head of the group
   uint32_t qf[kDim / 16][4];
   {
@@ -209,6 +220,8 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
       qf[s][1] = rb < p.group ? *reinterpret_cast<const uint32_t*>(qc + s * 32) : 0u;
       qf[s][2] = ra < p.group ? *reinterpret_cast<const uint32_t*>(qa + s * 32 + 16) : 0u;
       qf[s][3] = rb < p.group ? *reinterpret_cast<const uint32_t*>(qc + s * 32 + 16) : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qf[s][i] = (qf[s][i] ^ p.q_flip) & p.q_keep;
     }
   }
 
@@ -222,44 +235,79 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
   const int32_t first = int32_t(rank) * kGroups + grp;
   const int32_t mine = p.tiles > first ? (p.tiles - first + step - 1) / step : 0;   // tiles of this group
 
-  // Two loads lie between a list entry and its rows (the index, the page): each is fetched a tile ahead of its use.
-  auto entry = [&](int32_t i) {   // this lane's position in the group's tile i
-    return i < mine && lane < kAtTile ? list_position(p, idx, (first + i * step) * kAtTile + lane, end) : -1;
+  // Two loads lie between a list entry and its rows (the index, the page): each is fetched ahead of its use,
+  // 32 entries (one a lane) at a time.
+  constexpr int kBatch = 32 / kAtTile;     // tiles of a look-up
+  auto entry = [&](int32_t i) {            // this lane's position in the group's tiles i .. i + kBatch - 1
+    const int32_t tile = i + lane / kAtTile;
+    return tile < mine ? list_position(p, idx, (first + tile * step) * kAtTile + lane % kAtTile, end) : -1;
   };
   int32_t pos_next = entry(0);
+  Place at = {-1, 0};
+  uint32_t exist = 0u;                     // bit l: lane l's position of the look-up exists
+  int32_t slot = -1;
   constexpr int kPerPass = 32 / kPieces;   // rows that a warp copies at once
-  const int piece = lane % kPieces;
-  auto issue = [&](int32_t i) -> uint32_t {   // starts the copies of the group's tile i; which of its positions exist
-    if (i >= mine) return 0u;
-    const Place at = locate(p, table, pos_next);
-    pos_next = entry(i + 1);
-    const uint32_t any = __ballot_sync(0xFFFFFFFFu, at.page >= 0);
-    if (any == 0u) return 0u;
-    const uint32_t dst = ring + uint32_t(i % p.stages) * (2 * kTileBytes);
-    if (p.rows_even) {
-      const int32_t slot = at.page >= 0 ? at.page * p.page_size + at.row : -1;
+  constexpr uint32_t kFullTile = kAtTile == 32 ? 0xFFFFFFFFu : (1u << kAtTile) - 1u;
+  const int piece = lane % kPieces, my_row = rw * (kAtTile / kRowWarps) + lane / kPieces;
+  uint32_t put[4];                         // where a lane's piece of row my_row + kPerPass * j lies in a tile (j mod 4)
 #pragma unroll
-      for (int r = 0; r < kAtTile / kRowWarps; r += kPerPass) {
-        const int row = rw * (kAtTile / kRowWarps) + r + lane / kPieces;
-        const int32_t s = __shfl_sync(0xFFFFFFFFu, slot, row);
-        const uint32_t to = dst + uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4);
-        const int64_t o = int64_t(s < 0 ? 0 : s) * int32_t(p.k_row_bytes) + piece * 16;
-        copy16(to, kbase + o, s >= 0);
-        copy16(to + kTileBytes, vbase + o, s >= 0);
+  for (int j = 0; j < 4; ++j) {
+    const int row = my_row + kPerPass * j;
+    put[j] = uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4);
+  }
+  const uint8_t* kpiece = kbase + piece * 16;
+  const uint8_t* vpiece = vbase + piece * 16;
+  uint32_t fill = ring;                    // the stage that is filled next
+  const uint32_t ring_end = ring + uint32_t(p.stages) * (2 * kTileBytes);
+  auto issue = [&](int32_t i) -> uint32_t {   // starts the copies of the group's tile i; which of its positions exist
+    const uint32_t dst = fill;
+    fill += 2 * kTileBytes;
+    if (fill == ring_end) fill = ring;
+    if (i >= mine) return 0u;
+    const int sub = kBatch > 1 ? i % kBatch : 0;
+    if (sub == 0) {
+      at = locate(p, table, pos_next);
+      pos_next = entry(i + kBatch);
+      exist = __ballot_sync(0xFFFFFFFFu, at.page >= 0);
+      slot = at.page >= 0 ? at.page * p.page_size + at.row : -1;   // (used where it fits)
+    }
+    const uint32_t any = (exist >> (sub * kAtTile)) & kFullTile;
+    if (any == 0u) return 0u;
+    const int from = sub * kAtTile + my_row;   // the lane that knows this lane's first row
+    if (p.rows_even && any == kFullTile) {
+#pragma unroll
+      for (int j = 0; j < kAtTile / kRowWarps / kPerPass; ++j) {
+        const int32_t s = __shfl_sync(0xFFFFFFFFu, slot, from + kPerPass * j);
+        const int64_t o = int64_t(s) * int32_t(p.k_row_bytes);
+        const uint32_t to = dst + put[j & 3] + uint32_t((j >> 2) * 4 * kPerPass * kRowBytes);
+        copy16(to, kpiece + o);
+        copy16(to + kTileBytes, vpiece + o);
       }
     } else {
 #pragma unroll 2
-      for (int r = 0; r < kAtTile / kRowWarps; r += kPerPass) {
-        const int row = rw * (kAtTile / kRowWarps) + r + lane / kPieces;
-        const int64_t page = __shfl_sync(0xFFFFFFFFu, at.page, row), place = __shfl_sync(0xFFFFFFFFu, at.row, row);
+      for (int j = 0; j < kAtTile / kRowWarps / kPerPass; ++j) {
+        const int64_t page = __shfl_sync(0xFFFFFFFFu, at.page, from + kPerPass * j);
+        const int64_t place = __shfl_sync(0xFFFFFFFFu, at.row, from + kPerPass * j);
+        const int row = my_row + kPerPass * j;
         const uint32_t to = dst + uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4);
         const bool in = page >= 0;
-        copy16(to, kbase + (in ? page * p.k_page_bytes + place * p.k_row_bytes + piece * 16 : 0), in);
-        copy16(to + kTileBytes, vbase + (in ? page * p.v_page_bytes + place * p.v_row_bytes + piece * 16 : 0), in);
+        copy16(to, in ? kpiece + page * p.k_page_bytes + place * p.k_row_bytes : p.k, in);
+        copy16(to + kTileBytes, in ? vpiece + page * p.v_page_bytes + place * p.v_row_bytes : p.v, in);
       }
     }
     return any;
   };
+
+  // Where this lane's rows of the operand fragments lie in a tile: of keys for the product with q (rows as
+  // they are), of values for the product with the probabilities (transposed on the way); depth step d: j = d mod 4.
+  uint32_t key_at[4], value_at[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t kr = uint32_t((lane & 7) + ((lane >> 4) << 3)), vr = uint32_t(lane & 15);
+    key_at[j] = kr * kRowBytes + (((uint32_t(2 * j) + ((lane >> 3) & 1u)) ^ (lane & 7u)) << 4);
+    value_at[j] = kTileBytes + vr * kRowBytes + (((uint32_t(2 * j) + (uint32_t(lane) >> 4)) ^ (lane & 7u)) << 4);
+  }
+  constexpr float kNone = -__builtin_huge_valf();
 
   uint32_t live[kAtMaxStages];   // which positions of the tiles in flight exist
 #pragma unroll
@@ -269,6 +317,7 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
     if (s < p.stages - 1) live[s] = issue(s);
     copy_commit();
   }
+  uint32_t tile_at = ring;
   for (int32_t i = 0; i < mine; ++i) {
     // (with fewer than kAtMaxStages stages the ring is only that deep: the newest group is this tile's own)
     const uint32_t newest = issue(i + p.stages - 1);
@@ -284,47 +333,52 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
       copy_wait<0>();
     }
     group_sync<kRowWarps>(grp);
-    const uint32_t here = live[0];
+    const uint32_t here = live[0], kt = tile_at;
     live[0] = live[1];
     live[1] = live[2];
+    tile_at += 2 * kTileBytes;
+    if (tile_at == ring_end) tile_at = ring;
     if (here != 0u) {
-      const uint32_t kt = ring + uint32_t(i % p.stages) * (2 * kTileBytes);
-      const uint32_t vt = kt + kTileBytes;
-      float s[kAtTile / 8][4];
+      float s[kAtTile / 8][4], s2[kAtTile / 8][4];   // two sums of half the depth each: shorter chains
 #pragma unroll
-      for (int n = 0; n < kAtTile / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      for (int n = 0; n < kAtTile / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
       for (int d = 0; d < kDim / 16; ++d) {
 #pragma unroll
         for (int n = 0; n < kAtTile / 16; ++n) {   // 16 keys: two column tiles, both halves of the depth
-          const int row = n * 16 + (lane & 7) + ((lane >> 4) << 3);
-          const int piece = d * 2 + ((lane >> 3) & 1);
           uint32_t b[4];
-          ldmatrix4(kt + uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4), b);
-          mma16816<kBf16>(s[2 * n], qf[d], b[0], b[1]);
-          mma16816<kBf16>(s[2 * n + 1], qf[d], b[2], b[3]);
+          ldmatrix4(kt + key_at[d & 3] + uint32_t(n * 16 * kRowBytes + (d >> 2) * 128), b);
+          mma16816<kBf16>((d & 1) != 0 ? s2[2 * n] : s[2 * n], qf[d], b[0], b[1]);
+          mma16816<kBf16>((d & 1) != 0 ? s2[2 * n + 1] : s[2 * n + 1], qf[d], b[2], b[3]);
         }
       }
-      // scores as powers of two; positions that do not exist do not count
+#pragma unroll
+      for (int n = 0; n < kAtTile / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
+      if (here != kFullTile) {   // positions that do not exist do not count
+        const uint32_t cols = here >> ((lane & 3) * 2);
+#pragma unroll
+        for (int n = 0; n < kAtTile / 8; ++n) {
+          if (((cols >> (n * 8)) & 1u) == 0u) s[n][0] = s[n][2] = kNone;
+          if (((cols >> (n * 8 + 1)) & 1u) == 0u) s[n][1] = s[n][3] = kNone;
+        }
+      }
       float x0 = m0, x1 = m1;
-      const uint32_t cols = here >> ((lane & 3) * 2);
 #pragma unroll
       for (int n = 0; n < kAtTile / 8; ++n) {
-        const bool c0 = (cols >> (n * 8)) & 1u, c1 = (cols >> (n * 8 + 1)) & 1u;
-        s[n][0] = c0 ? s[n][0] * p.scale_log2 : -__int_as_float(0x7F800000);
-        s[n][1] = c1 ? s[n][1] * p.scale_log2 : -__int_as_float(0x7F800000);
-        s[n][2] = c0 ? s[n][2] * p.scale_log2 : -__int_as_float(0x7F800000);
-        s[n][3] = c1 ? s[n][3] * p.scale_log2 : -__int_as_float(0x7F800000);
         x0 = fmaxf(x0, fmaxf(s[n][0], s[n][1]));
         x1 = fmaxf(x1, fmaxf(s[n][2], s[n][3]));
       }
       x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 2));
       x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
+      x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 2));
       x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 2));
       if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
         // (a row without a score so far has m = -inf and holds zeros: any factor is right, but -inf - -inf is not one)
-        const float f0 = x0 == m0 ? 1.f : pow2(m0 - x0), f1 = x1 == m1 ? 1.f : pow2(m1 - x1);
+        const float f0 = x0 == m0 ? 1.f : pow2((m0 - x0) * p.scale_log2), f1 = x1 == m1 ? 1.f : pow2((m1 - x1) * p.scale_log2);
         l0 *= f0;
         l1 *= f1;
 #pragma unroll
@@ -337,13 +391,14 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
         m0 = x0;
         m1 = x1;
       }
-      const float z0 = m0 == -__int_as_float(0x7F800000) ? 0.f : m0, z1 = m1 == -__int_as_float(0x7F800000) ? 0.f : m1;
+      // (product - maximum) * scale: the difference of two products is exact where it matters, near the maximum
+      const float z0 = m0 == kNone ? 0.f : m0, z1 = m1 == kNone ? 0.f : m1;
 #pragma unroll
       for (int n = 0; n < kAtTile / 8; ++n) {
-        s[n][0] = pow2(s[n][0] - z0);
-        s[n][1] = pow2(s[n][1] - z0);
-        s[n][2] = pow2(s[n][2] - z1);
-        s[n][3] = pow2(s[n][3] - z1);
+        s[n][0] = pow2((s[n][0] - z0) * p.scale_log2);
+        s[n][1] = pow2((s[n][1] - z0) * p.scale_log2);
+        s[n][2] = pow2((s[n][2] - z1) * p.scale_log2);
+        s[n][3] = pow2((s[n][3] - z1) * p.scale_log2);
         l0 += s[n][0] + s[n][1];
         l1 += s[n][2] + s[n][3];
       }
@@ -354,10 +409,8 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
                                pack16<kBf16>(s[2 * n + 1][2], s[2 * n + 1][3])};
 #pragma unroll
         for (int d = 0; d < kDim / 16; ++d) {
-          const int row = n * 16 + (lane & 15);
-          const int piece = d * 2 + (lane >> 4);
           uint32_t b[4];
-          ldmatrix4t(vt + uint32_t(row) * kRowBytes + (uint32_t(piece ^ (row & 7)) << 4), b);
+          ldmatrix4t(kt + value_at[d & 3] + uint32_t(n * 16 * kRowBytes + (d >> 2) * 128), b);
           mma16816<kBf16>(o[2 * d], a, b[0], b[1]);
           mma16816<kBf16>(o[2 * d + 1], a, b[2], b[3]);
         }
@@ -409,7 +462,7 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
     float sum = 0.f;
     for (int i = 0; i < parts; ++i) {
       const float li = peer_load(peer_addr(shared_addr(ml + ((i % kGroups) * kRows + r) * 2 + 1), uint32_t(i / kGroups)));
-      const float w = pow2(wt[i * kRows + r] - z);
+      const float w = pow2((wt[i * kRows + r] - z) * p.scale_log2);
       wt[i * kRows + r] = w;
       sum += li * w;
     }
@@ -417,7 +470,7 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
     const int head = rt * kRows + r;
     if (rank == 0 && p.lse != nullptr && head < p.group)
       p.lse[int64_t(t) * p.kv_heads * p.group + kvh * p.group + head] =
-          sum == 0.f ? -__int_as_float(0x7F800000) : (z + log2f(sum)) * 0.6931471805599453f;
+          sum == 0.f ? -__int_as_float(0x7F800000) : (z * p.scale_log2 + log2f(sum)) * 0.6931471805599453f;
   }
   __syncthreads();
   for (int i = int(rank) * kAtThreads + int(threadIdx.x); i < kRows * kDim / 4; i += int(ranks) * kAtThreads) {
@@ -540,7 +593,13 @@ DSEL_API int dsel_sparse_attn(const void* q, int dtype, int64_t tokens, int32_t 
   p.end = end;
   p.out = out;
   p.lse = lse;
-  p.scale_log2 = float(double(scale) * 1.4426950408889634);
+  p.scale_log2 = float((scale < 0 ? -double(scale) : double(scale)) * 1.4426950408889634);
+  p.q_flip = scale < 0 ? 0x80008000u : 0u;
+  p.q_keep = 0xFFFFFFFFu;
+  if (p.scale_log2 == 0.f) {   // -inf, the score of what does not exist, takes no factor of 0
+    p.scale_log2 = 1.f;
+    p.q_keep = 0u;
+  }
   p.pages = pages;
   p.page_size = page_size;
   p.page_shift = log2_of(page_size);
