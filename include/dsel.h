@@ -316,7 +316,8 @@ DSEL_API int dsel_take_index(const int64_t* table, int64_t table_stride, const v
  *   3. y = y + the row's biases of v (an entry that occurs twice counts twice)
  *   4. y = -inf where the row's mask has a 0 at v, whatever y was (NaN too)
  *   out[r][v] = y; out[r][vocab .. out_stride) = -inf
- * in float32, biases in list order: the result does not depend on scheduling.
+ * in float32 (1: a product with the rounded reciprocal; 2: one sum of the two penalties),
+ * biases in list order: the result does not depend on scheduling.
  * A row whose mask leaves nothing holds only -inf (dsel_topk_sample then draws
  * uniformly among its first k).
  *
@@ -329,7 +330,8 @@ DSEL_API int dsel_take_index(const int64_t* table, int64_t table_stride, const v
  *                them).  Ids outside [0, vocab) are ignored.
  *   repetition, frequency, presence
  *                device float32 [rows], each may be NULL: 1, 0, 0.  The tokens of a
- *                row with neutral values are not read.
+ *                row with neutral values are not read.  repetition[r] and its reciprocal
+ *                are meant to be normal float32 numbers.
  *   bias_offsets, bias_ids, bias_values, bias_count
  *                row r's biases are the entries bias_offsets[r] .. bias_offsets[r + 1]
  *                (int32 [rows + 1], clamped to [0, bias_count]) of int32 ids and float32

@@ -41,7 +41,7 @@ def oracle_logits(x, stride, *, tokens=None, prompt_len=None, total_len=None, re
                 for v in seen:
                     z[v] = z[v] / rep if z[v] > 0 else z[v] * rep
                     m[v] = max(m[v], abs(z[v]))
-                    n[v] += 1
+                    n[v] += 2.001     # the reciprocal and the product: (1 + e)^2 - 1 < 2.001 e for e = 2^-24
                 for v, c in count.items():
                     z[v] -= freq * c + pres
                     m[v] += abs(freq * c) + abs(pres)

@@ -25,7 +25,7 @@
 namespace dsel {
 namespace {
 
-constexpr int kLgThreads = 512;
+constexpr int kLgThreads = 256;
 constexpr int kLgVecs = 4;                            // vectors of 4 elements each thread holds
 constexpr int kLgSlice = kLgThreads * kLgVecs * 4;    // vocabulary entries of a CTA
 constexpr uint32_t kInPrompt = 0x80000000u;           // count word: seen in the prompt; low bits: answer count
@@ -70,27 +70,62 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// Counts the row's tokens [from, to) that fall in the slice [base, base + kLgSlice).
-template <typename tok_t>
-__device__ __forceinline__ void count_tokens(const tok_t* __restrict__ t, int32_t to, int32_t prompt, int32_t base,
-                                             int32_t slice_end, uint32_t* counts) {
+// Counts the row's first `to` tokens that fall in [base, base + len).  Each CTA of a row scans them all, so a
+// token costs a quarter of a load, a subtraction and a comparison.
+struct Counter {
+  uint32_t* counts;
+  int32_t base;
+  uint32_t len;
+  int32_t prompt;
+  __device__ __forceinline__ void add(int32_t id, int32_t i) const {
+    const uint32_t d = uint32_t(id) - uint32_t(base);   // (an id below base, or negative, wraps past len)
+    if (d < len) {
+      if (i < prompt)
+        atomicOr(&counts[d], kInPrompt);
+      else
+        atomicAdd(&counts[d], 1u);
+    }
+  }
+  __device__ __forceinline__ void add(int64_t id, int32_t i) const {
+    if (id >= 0 && id <= INT32_MAX) add(int32_t(id), i);
+  }
+};
+
+__device__ __forceinline__ void count_tokens(const int64_t* __restrict__ t, int32_t to, const Counter& c) {
   constexpr int kUnroll = 8;
-  for (int32_t i0 = 0; i0 < to; i0 += kLgThreads * kUnroll) {
+  for (int32_t i0 = int32_t(threadIdx.x); i0 < to; i0 += kLgThreads * kUnroll) {
     int64_t id[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int32_t i = i0 + u * kLgThreads + int32_t(threadIdx.x);
-      id[u] = i < to ? int64_t(t[i]) : -1;
-    }
+    for (int u = 0; u < kUnroll; ++u) id[u] = i0 + u * kLgThreads < to ? t[i0 + u * kLgThreads] : -1;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) c.add(id[u], i0 + u * kLgThreads);
+  }
+}
+
+__device__ __forceinline__ void count_tokens(const int32_t* __restrict__ t, int32_t to, const Counter& c) {
+  constexpr int kUnroll = 4;
+  const int32_t off = int32_t((16u - (reinterpret_cast<uintptr_t>(t) & 15u)) & 15u) / 4;   // up to a 16-byte boundary
+  const int32_t head = off < to ? off : to;
+  const int32_t quads = (to - head) / 4, tail = head + quads * 4;
+  const int32_t tid = int32_t(threadIdx.x);
+  if (tid < head) c.add(t[tid], tid);
+  if (tid < to - tail) c.add(t[tail + tid], tail + tid);
+  const int4* q = reinterpret_cast<const int4*>(t + head);
+  for (int32_t i0 = tid; i0 < quads; i0 += kLgThreads * kUnroll) {
+    int4 id[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      id[u] = i0 + u * kLgThreads < quads ? q[i0 + u * kLgThreads] : make_int4(-1, -1, -1, -1);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (id[u] >= base && id[u] < slice_end) {
-        const int32_t i = i0 + u * kLgThreads + int32_t(threadIdx.x);
-        if (i < prompt)
-          atomicOr(&counts[id[u] - base], kInPrompt);
-        else
-          atomicAdd(&counts[id[u] - base], 1u);
-      }
+      const uint32_t dx = uint32_t(id[u].x) - uint32_t(c.base), dy = uint32_t(id[u].y) - uint32_t(c.base);
+      const uint32_t dz = uint32_t(id[u].z) - uint32_t(c.base), dw = uint32_t(id[u].w) - uint32_t(c.base);
+      if (min(min(dx, dy), min(dz, dw)) >= c.len) continue;   // none of the four is in the slice
+      const int32_t i = head + (i0 + u * kLgThreads) * 4;
+      c.add(id[u].x, i);
+      c.add(id[u].y, i + 1);
+      c.add(id[u].z, i + 2);
+      c.add(id[u].w, i + 3);
     }
   }
 }
@@ -111,7 +146,18 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(const __grid_constan
   }
   grid_wait();   // nothing above touches global memory
 
-  // the slice's logits, loaded before anything waits
+  // the row's numbers, then the slice's logits: all on their way before anything is waited for
+  const float rep = p.repetition != nullptr ? p.repetition[row] : 1.f;
+  const float freq = p.frequency != nullptr ? p.frequency[row] : 0.f;
+  const float pres = p.presence != nullptr ? p.presence[row] : 0.f;
+  int32_t total = p.total_len != nullptr ? p.total_len[row] : p.width;
+  const int32_t prompt = p.prompt_len != nullptr ? p.prompt_len[row] : 0;
+  int64_t mrow = -1, b0 = 0, b1 = 0;
+  if (p.mask != nullptr) mrow = p.mask_rows != nullptr ? int64_t(p.mask_rows[row]) : row;
+  if (p.bias_ids != nullptr) {
+    b0 = p.bias_offsets[row];
+    b1 = p.bias_offsets[row + 1];
+  }
   const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
   float4 y[kLgVecs];
 #pragma unroll
@@ -128,8 +174,6 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(const __grid_constan
   }
   // the mask's words of those vectors (bits of one vector lie in one word)
   uint32_t allowed[kLgVecs];
-  int64_t mrow = -1;
-  if (p.mask != nullptr) mrow = p.mask_rows != nullptr ? int64_t(p.mask_rows[row]) : row;
   const bool masked = mrow >= 0 && mrow < p.mask_count;
 #pragma unroll
   for (int j = 0; j < kLgVecs; ++j) {
@@ -140,26 +184,18 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(const __grid_constan
     if (left < 4) allowed[j] &= left > 0 ? (1u << left) - 1u : 0u;
   }
 
-  const float rep = p.repetition != nullptr ? p.repetition[row] : 1.f;
-  const float freq = p.frequency != nullptr ? p.frequency[row] : 0.f;
-  const float pres = p.presence != nullptr ? p.presence[row] : 0.f;
+  // A positive logit is divided as a product with the reciprocal: two roundings for one, but a division for
+  // each element took a third of the kernel's instructions.
+  const float inverse = 1.f / rep;
   const int32_t slice_end = p.vocab - base < kLgSlice ? p.vocab : base + kLgSlice;
-  __syncthreads();   // the count words are zero
+  b0 = b0 < 0 ? 0 : b0;
+  b1 = b1 > p.bias_count ? p.bias_count : b1;
+  const bool biased = b0 < b1;
   // neutral penalties change no logit, so such a row's tokens are not read
   const bool counted = p.tokens != nullptr && (rep != 1.f || freq != 0.f || pres != 0.f) && base < p.vocab;
-  if (counted) {
-    int32_t total = p.total_len != nullptr ? p.total_len[row] : p.width;
-    total = total < 0 ? 0 : (total > p.width ? p.width : total);
-    const int32_t prompt = p.prompt_len != nullptr ? p.prompt_len[row] : 0;
-    count_tokens(static_cast<const tok_t*>(p.tokens) + row * p.tokens_stride, total, prompt, base, slice_end, counts);
-  }
+  __syncthreads();   // the count words are zero
   // biases: one warp walks the row's list, so repeated entries add up in list order
-  bool biased = false;
-  if (p.bias_ids != nullptr) {
-    int64_t b0 = p.bias_offsets[row], b1 = p.bias_offsets[row + 1];
-    b0 = b0 < 0 ? 0 : b0;
-    b1 = b1 > p.bias_count ? p.bias_count : b1;
-    biased = b0 < b1;
+  if (biased) {
     if (tid < 32) {
       for (int64_t b = b0; b < b1; b += 32) {
         const bool in = b + tid < b1;
@@ -181,6 +217,11 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(const __grid_constan
       }
     }
   }
+  if (counted) {
+    total = total < 0 ? 0 : (total > p.width ? p.width : total);
+    const Counter c = {counts, base, uint32_t(slice_end - base), prompt};
+    count_tokens(static_cast<const tok_t*>(p.tokens) + row * p.tokens_stride, total, c);
+  }
   __syncthreads();
   grid_launch();   // a dependent launch may begin its own set-up
 
@@ -195,13 +236,13 @@ __global__ void __launch_bounds__(kLgThreads) logits_kernel(const __grid_constan
     if (counted) {
       const uint4 c4 = *reinterpret_cast<const uint4*>(counts + o);
       const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
-      if ((c4.x | c4.y | c4.z | c4.w) != 0u) {
+      if ((c4.x | c4.y | c4.z | c4.w) != 0u) {   // few: but some lane of a warp mostly has one, so no branches within
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (c[i] == 0u) continue;
-          v[i] = v[i] > 0.f ? __fdiv_rn(v[i], rep) : v[i] * rep;
           const uint32_t n = c[i] & ~kInPrompt;
-          if (n != 0u) v[i] = v[i] - freq * float(n) - pres;
+          const float seen = v[i] * (v[i] > 0.f ? inverse : rep);
+          const float less = n != 0u ? freq * float(n) + pres : 0.f;
+          v[i] = c[i] != 0u ? seen - less : v[i];
         }
       }
     }
@@ -246,7 +287,7 @@ DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, 
     return DSEL_ERR_STRIDE;
   if (tokens != nullptr) {
     if (token_dtype != DSEL_I32 && token_dtype != DSEL_I64) return DSEL_ERR_INDEX_DTYPE;
-    if (width < 0 || width > INT32_MAX - 8 * kLgThreads) return DSEL_ERR_SHAPE;
+    if (width < 0 || width > INT32_MAX - 16 * kLgThreads) return DSEL_ERR_SHAPE;
     if (tokens_stride < width) return DSEL_ERR_STRIDE;
   }
   if (bias_count < 0 || mask_count < 0) return DSEL_ERR_SHAPE;
