@@ -176,7 +176,7 @@ __device__ __forceinline__ Place locate(const AttnParams& p, const int32_t* tabl
 }
 
 template <bool kBf16, int kDim, int kRowWarps>
-__global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kAtThreads, kRowWarps == 1 ? 3 : 1) attn_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kGroups = kAtWarps / kRowWarps;          // key groups of the CTA
   constexpr int kRows = 16 * kRowWarps;                  // query heads of the CTA
@@ -339,25 +339,30 @@ __global__ void __launch_bounds__(kAtThreads) attn_kernel(const __grid_constant_
     tile_at += 2 * kTileBytes;
     if (tile_at == ring_end) tile_at = ring;
     if (here != 0u) {
-      float s[kAtTile / 8][4], s2[kAtTile / 8][4];   // two sums of half the depth each: shorter chains
+      constexpr bool kSplit = kAtTile == 16;   // two sums of half the depth each: shorter chains where there are few
+      float s[kAtTile / 8][4], s2[kSplit ? kAtTile / 8 : 1][4];
 #pragma unroll
       for (int n = 0; n < kAtTile / 8; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] = 0.f;
+          if (kSplit) s2[n][e] = 0.f;
+        }
 #pragma unroll
       for (int d = 0; d < kDim / 16; ++d) {
 #pragma unroll
         for (int n = 0; n < kAtTile / 16; ++n) {   // 16 keys: two column tiles, both halves of the depth
           uint32_t b[4];
           ldmatrix4(kt + key_at[d & 3] + uint32_t(n * 16 * kRowBytes + (d >> 2) * 128), b);
-          mma16816<kBf16>((d & 1) != 0 ? s2[2 * n] : s[2 * n], qf[d], b[0], b[1]);
-          mma16816<kBf16>((d & 1) != 0 ? s2[2 * n + 1] : s[2 * n + 1], qf[d], b[2], b[3]);
+          mma16816<kBf16>(kSplit && (d & 1) != 0 ? s2[2 * n] : s[2 * n], qf[d], b[0], b[1]);
+          mma16816<kBf16>(kSplit && (d & 1) != 0 ? s2[2 * n + 1] : s[2 * n + 1], qf[d], b[2], b[3]);
         }
       }
 #pragma unroll
       for (int n = 0; n < kAtTile / 8; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
+        for (int e = 0; e < 4; ++e)
+          if (kSplit) s[n][e] += s2[n][e];
       if (here != kFullTile) {   // positions that do not exist do not count
         const uint32_t cols = here >> ((lane & 3) * 2);
 #pragma unroll
