@@ -314,5 +314,15 @@ def topk_sample(logits, k: int, u, *, temperature: float = 1.0, top_p: float = 1
     return token, prob
 
 
-# the operators before and after the selection (same manner: torch tensors in, one library call)
-from .serving import index_score, process_logits, sparse_attention  # noqa: E402,F401
+# The operators before and after the selection: same manner, torch tensors in, one library call.  They load on
+# first use, so that the package itself does not import torch.
+_SERVING = ("index_score", "process_logits", "sparse_attention")
+
+
+def __getattr__(name):
+    if name in _SERVING:
+        from . import serving
+        for n in _SERVING:
+            globals()[n] = getattr(serving, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -19,6 +19,8 @@ from __future__ import annotations
 
 import struct
 
+import torch
+
 from . import (DSEL_BF16, DSEL_CALL_INDEX_SCORE, DSEL_CALL_LOGITS, DSEL_CALL_SPARSE_ATTN, DSEL_E4M3, DSEL_F16, DSEL_F32,
                DSEL_I32, DSEL_I64, DSEL_OK, DselError, lib)
 
@@ -28,17 +30,19 @@ _SCORE = struct.Struct("=26q")
 _ATTN = struct.Struct("=30qd3q")
 
 _call = lib.dsel_call
+_stream_of = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_I32, _I64, _F32, _BF16, _F16, _E4M3 = (torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.float16,
+                                        torch.float8_e4m3fn)
 
 
 def _run(device, stream, call):
     """``call(stream handle)`` with CUDA device `device` current and, for a given stream, as torch's current one."""
-    import torch
-
-    if stream is None and torch._C._cuda_getDevice() == device:
-        return call(torch._C._cuda_getCurrentRawStream(device))
+    if stream is None and _current_device() == device:
+        return call(_stream_of(device))
     with torch.cuda.device(device):
         if stream is None:
-            return call(torch._C._cuda_getCurrentRawStream(device))
+            return call(_stream_of(device))
         with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
             return call(stream)
 
@@ -70,11 +74,9 @@ def _rows_of(name, t, device, rows):
 
 
 def _index_dtype(name, t):
-    import torch
-
-    if t.dtype is torch.int32:
+    if t.dtype is _I32:
         return DSEL_I32
-    if t.dtype is torch.int64:
+    if t.dtype is _I64:
         return DSEL_I64
     raise TypeError(f"{name} must be int32 or int64")
 
@@ -96,15 +98,12 @@ def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repe
     with -inf in the columns behind the vocabulary.  ``out`` may supply that tensor; it
     may be ``logits`` itself when that is float32, contiguous and of such a width.
     """
-    import torch
-
-    f32, i32 = torch.float32, torch.int32
     dev = logits.get_device()
     if dev < 0 or logits.dim() != 2:
         raise ValueError("logits must be a 2-D CUDA tensor [rows, vocab] (there is no CPU path)")
-    if logits.dtype is torch.bfloat16:
+    if logits.dtype is _BF16:
         dt = DSEL_BF16
-    elif logits.dtype is f32:
+    elif logits.dtype is _F32:
         dt = DSEL_F32
     else:
         raise TypeError("logits must be bfloat16 or float32")
@@ -121,28 +120,28 @@ def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repe
     elif not (prompt_len is None and total_len is None and repetition is None and frequency is None
               and presence is None):
         raise ValueError("penalties and lengths need tokens=")
-    p_prompt = _vector("prompt_len", prompt_len, dev, i32, rows)
-    p_total = _vector("total_len", total_len, dev, i32, rows)
-    p_rep = _vector("repetition", repetition, dev, f32, rows)
-    p_freq = _vector("frequency", frequency, dev, f32, rows)
-    p_pres = _vector("presence", presence, dev, f32, rows)
+    p_prompt = _vector("prompt_len", prompt_len, dev, _I32, rows)
+    p_total = _vector("total_len", total_len, dev, _I32, rows)
+    p_rep = _vector("repetition", repetition, dev, _F32, rows)
+    p_freq = _vector("frequency", frequency, dev, _F32, rows)
+    p_pres = _vector("presence", presence, dev, _F32, rows)
     p_boff = p_bids = p_bval = n_bias = 0
     if bias_ids is not None or bias_offsets is not None or bias_values is not None:
         if bias_ids is None or bias_offsets is None or bias_values is None:
             raise ValueError("bias_offsets, bias_ids and bias_values come together")
         n_bias = bias_ids.shape[0] if bias_ids.dim() == 1 else -1
-        p_bids = _vector("bias_ids", bias_ids, dev, i32, n_bias)
-        p_bval = _vector("bias_values", bias_values, dev, f32, n_bias)
-        p_boff = _vector("bias_offsets", bias_offsets, dev, i32, rows + 1)
+        p_bids = _vector("bias_ids", bias_ids, dev, _I32, n_bias)
+        p_bval = _vector("bias_values", bias_values, dev, _F32, n_bias)
+        p_boff = _vector("bias_offsets", bias_offsets, dev, _I32, rows + 1)
         if n_bias == 0:
             p_boff = p_bids = p_bval = 0
     p_mask = m_stride = m_count = p_mrows = 0
     if mask is not None:
-        if mask.dtype is not i32:
+        if mask.dtype is not _I32:
             raise TypeError("mask must be int32 words")
         m_stride = _rows_of("mask", mask, dev, None)
         m_count, words = mask.shape
-        p_mrows = _vector("mask_rows", mask_rows, dev, i32, rows)
+        p_mrows = _vector("mask_rows", mask_rows, dev, _I32, rows)
         if words * 32 < vocab:
             raise ValueError("mask rows must hold a bit for every token")
         if mask_rows is None and m_count < rows:
@@ -151,12 +150,12 @@ def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repe
             p_mask = mask.data_ptr()
     elif mask_rows is not None:
         raise ValueError("mask_rows needs mask=")
-    if out is not None and (out.dtype is not f32 or out.get_device() != dev or out.dim() != 2 or out.shape[0] != rows
+    if out is not None and (out.dtype is not _F32 or out.get_device() != dev or out.dim() != 2 or out.shape[0] != rows
                             or out.shape[1] < vocab or out.shape[1] % 16 or not out.is_contiguous()):
         raise ValueError("out must be a contiguous float32 tensor [rows, n], n >= vocab a multiple of 16")
 
     def call(handle):
-        o = out if out is not None else logits.new_empty((rows, vocab + 15 & ~15), dtype=f32)
+        o = out if out is not None else logits.new_empty((rows, vocab + 15 & ~15), dtype=_F32)
         status = _call(DSEL_CALL_LOGITS, _LOGITS.pack(
             logits.data_ptr(), dt, rows, vocab, x_stride, p_tokens, t_dt, width, t_stride, p_prompt, p_total, p_rep,
             p_freq, p_pres, p_boff, p_bids, p_bval, n_bias, p_mask, m_stride, m_count, p_mrows, o.data_ptr(),
@@ -170,36 +169,32 @@ def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repe
 
 def _operand_dtype(name, t, byte):
     """The DSEL code of a 16-bit operand (or, where `byte`, of an e4m3 one)."""
-    import torch
-
-    if t.dtype is torch.bfloat16:
+    if t.dtype is _BF16:
         return DSEL_BF16
-    if t.dtype is torch.float16:
+    if t.dtype is _F16:
         return DSEL_F16
-    if byte and t.dtype is torch.float8_e4m3fn:
+    if byte and t.dtype is _E4M3:
         return DSEL_E4M3
     raise TypeError(f"{name} must be bfloat16" + (", float16 or float8_e4m3fn" if byte else " or float16"))
 
 
 def _queries(q, table, end, seq_ids):
     """Checks what every query of a paged cache comes with: (device, tokens, table stride, address of end, of seq_ids)."""
-    import torch
-
     dev = q.get_device()
     if dev < 0 or q.dim() != 3:
         raise ValueError("q must be a 3-D CUDA tensor [tokens, heads, dim] (there is no CPU path)")
     tokens = q.shape[0]
     if q.stride(2) != 1:
         raise ValueError("q must be contiguous in its last dimension")
-    if table.dtype is not torch.int32:
+    if table.dtype is not _I32:
         raise TypeError("block_table must be int32")
     t_stride = _rows_of("block_table", table, dev, None)
     if end is None:
         raise ValueError("end (the keys each query sees) must be given")
-    p_end = _vector("end", end, dev, torch.int32, tokens)
+    p_end = _vector("end", end, dev, _I32, tokens)
     p_seq = 0
     if seq_ids is not None:
-        p_seq = _vector("seq_ids", seq_ids, dev, torch.int32, tokens)
+        p_seq = _vector("seq_ids", seq_ids, dev, _I32, tokens)
     elif table.shape[0] != 1 and table.shape[0] != tokens:
         raise ValueError("block_table needs one row, or one for each query, or seq_ids=")
     return dev, tokens, t_stride, p_end, p_seq
@@ -220,23 +215,20 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
     sees no key; ``row_stride`` defaults to the keys a table row can name, rounded up to the
     TopK row-stride requirement.  ``out`` may supply that tensor.
     """
-    import torch
-
-    f32 = torch.float32
     dt = _operand_dtype("q", q, True)
     dev, tokens, t_stride, p_end, p_seq = _queries(q, block_table, end, seq_ids)
     _, heads, dim = q.shape
     if (keys.dtype is not q.dtype or keys.get_device() != dev or keys.dim() != 3 or keys.shape[2] != dim
             or keys.stride(2) != 1):
         raise ValueError("keys must be [pages, page_size, dim] of q's type on its device, contiguous in the last dimension")
-    if weights.dtype is not f32 or weights.shape != (tokens, heads):
+    if weights.dtype is not _F32 or weights.shape != (tokens, heads):
         raise ValueError("weights must be float32 [tokens, heads]")
     w_stride = _rows_of("weights", weights, dev, tokens)
     pages, page, _ = keys.shape
     k_page, k_row, _ = keys.stride()
     p_scale = s_stride = 0
     if key_scale is not None:
-        if key_scale.dtype is not f32 or key_scale.shape != (pages, page):
+        if key_scale.dtype is not _F32 or key_scale.shape != (pages, page):
             raise ValueError("key_scale must be float32 [pages, page_size]")
         s_stride = _rows_of("key_scale", key_scale, dev, pages)
         p_scale = key_scale.data_ptr()
@@ -251,8 +243,8 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
         if row_stride is None:
             row_stride = t_width * page + 15 & ~15
         if out_dtype is None:
-            out_dtype = torch.bfloat16
-    if out_dtype is not torch.bfloat16 and out_dtype is not f32:
+            out_dtype = _BF16
+    if out_dtype is not _BF16 and out_dtype is not _F32:
         raise TypeError("scores are bfloat16 or float32")
 
     def call(handle):
@@ -261,7 +253,7 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
         status = _call(DSEL_CALL_INDEX_SCORE, _SCORE.pack(
             q.data_ptr(), dt, tokens, heads, dim, q_token, q_head, weights.data_ptr(), w_stride, keys.data_ptr(),
             pages, page, k_page, k_row, p_scale, s_stride, block_table.data_ptr(), seqs, t_width, t_stride, p_seq,
-            p_end, o.data_ptr(), DSEL_F32 if out_dtype is f32 else DSEL_BF16, row_stride, handle))
+            p_end, o.data_ptr(), DSEL_F32 if out_dtype is _F32 else DSEL_BF16, row_stride, handle))
         if status != DSEL_OK:
             raise DselError(status)
         return o
@@ -284,8 +276,6 @@ def sparse_attention(q, k_cache, v_cache, block_table, indices, end, *, block=1,
     Returns [tokens, q_heads, dim] (``out`` may supply it), and with ``return_lse`` also the
     float32 logarithms of the sums of exponentials [tokens, q_heads].
     """
-    import torch
-
     dt = _operand_dtype("q", q, False)
     dev, tokens, t_stride, p_end, p_seq = _queries(q, block_table, end, seq_ids)
     _, heads, dim = q.shape
@@ -317,7 +307,7 @@ def sparse_attention(q, k_cache, v_cache, block_table, indices, end, *, block=1,
 
     def call(handle):
         o = out if out is not None else q.new_empty((tokens, heads, dim))
-        lse = q.new_empty((tokens, heads), dtype=torch.float32) if return_lse else None
+        lse = q.new_empty((tokens, heads), dtype=_F32) if return_lse else None
         q_token, q_head, _ = q.stride()
         seqs, t_width = block_table.shape
         status = _call(DSEL_CALL_SPARSE_ATTN, _ATTN.pack(
