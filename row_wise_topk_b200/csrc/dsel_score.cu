@@ -875,7 +875,7 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
   if (heads < 1 || heads > 128 || dim < 32 || dim > 128 || dim % 32 != 0) return DSEL_ERR_SHAPE;
   if (pages < 0 || page_size < 1 || seqs < 0 || table_width < 0) return DSEL_ERR_SHAPE;
   if (seq_ids == nullptr && seqs != 1 && int64_t(seqs) != tokens) return DSEL_ERR_SHAPE;
-  if (row_stride < 1 || row_stride % kStrideReq != 0 || row_stride > INT32_MAX - 64 * kTile) return DSEL_ERR_STRIDE;
+  if (row_stride < 1 || row_stride % kStrideReq != 0 || row_stride > INT32_MAX - 1024 * kTile) return DSEL_ERR_STRIDE;
   if (q_head_stride < dim || (tokens > 1 && q_token_stride < dim) || weights_stride < heads || key_stride < dim || page_stride < 0 ||
       table_stride < table_width || scale_page_stride < 0)
     return DSEL_ERR_STRIDE;

@@ -147,6 +147,27 @@ def test_strides():
     check(T.index_score(q, w, keys, table, d["end"], key_scale=scale), a)
 
 
+@pytest.mark.parametrize("page", [16, 12])
+@pytest.mark.parametrize("tokens", [1, 7])
+def test_layouts(page, tokens):
+    # heads before tokens, places before pages, a broadcast query
+    a = make(page + tokens, tokens=tokens, heads=6, dim=64, page=page, width=12, ends=[12 * page - i for i in range(tokens)])
+    d = {k: v.cuda() for k, v in a.items()}
+    q = d["q"].permute(1, 0, 2).contiguous().permute(1, 0, 2)
+    keys = d["keys"].permute(1, 0, 2).contiguous().permute(1, 0, 2)
+    assert tokens == 1 or not q.is_contiguous()
+    args = (d["weights"], keys, d["block_table"], d["end"])
+    check(T.index_score(q, *args), a)
+    if tokens > 1:
+        with pytest.raises(T.DselError):          # queries may not overlap
+            T.index_score(d["q"][:1].expand(tokens, 6, 64), *args)
+
+
+def test_default_stream_by_its_handle():
+    a = make(3, tokens=2, heads=4, dim=64, ends=[100, 128])
+    check(run(a, stream=torch.cuda.default_stream().cuda_stream), a)
+
+
 def test_special_values():
     a = make(13, tokens=3, heads=5, dim=32, page=16, width=16, ends=[256, 256, 100])
     a["keys"][a["block_table"][0, 2], 3, 7] = float("nan")

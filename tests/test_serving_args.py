@@ -79,6 +79,7 @@ def score(**kw):
     (dict(seqs=3), "DSEL_ERR_SHAPE"),            # neither one sequence nor one for each query
     (dict(row_stride=72), "DSEL_ERR_STRIDE"),
     (dict(row_stride=0), "DSEL_ERR_STRIDE"),
+    (dict(row_stride=(1 << 31) - 65536), "DSEL_ERR_STRIDE"),
     (dict(q_head_stride=32), "DSEL_ERR_STRIDE"),
     (dict(q_head_stride=68), "DSEL_ERR_STRIDE"),     # not 16 bytes
     (dict(q_token_stride=516), "DSEL_ERR_STRIDE"),
@@ -143,3 +144,19 @@ def test_attn_refusals(kw, err):
 
 def test_attn_zero_tokens_is_a_noop():
     assert attn(tokens=0, q=None, out=None, seqs=0) == T.DSEL_OK
+
+
+def test_packed_calls():
+    import struct
+    words = struct.pack("=25q", *([0x1000, T.DSEL_F32, -1] + [0] * 22))
+    assert T.lib.dsel_call(T.DSEL_CALL_LOGITS, words) == header_define("DSEL_ERR_ROWS")
+    words = struct.pack("=25q", *([0x1000, 1 << 40, 4] + [0] * 22))           # a dtype that no int holds
+    assert T.lib.dsel_call(T.DSEL_CALL_LOGITS, words) == header_define("DSEL_ERR_SHAPE")
+    words = struct.pack("=30qd3q", *([0x1000, T.DSEL_BF16, 0, 8, 3] + [0] * 25), 0.5, 0, 0, 0)
+    assert T.lib.dsel_call(T.DSEL_CALL_SPARSE_ATTN, words) == header_define("DSEL_ERR_SHAPE")
+    words = struct.pack("=26q", *([0x1000, T.DSEL_F32] + [0] * 24))
+    assert T.lib.dsel_call(T.DSEL_CALL_INDEX_SCORE, words) == header_define("DSEL_ERR_DTYPE")
+    assert T.lib.dsel_call(T.DSEL_CALL_LOGITS, None) == header_define("DSEL_ERR_NULL")
+    assert T.lib.dsel_call(3, words) == header_define("DSEL_ERR_UNAVAILABLE")
+    for name in ("DSEL_CALL_LOGITS", "DSEL_CALL_INDEX_SCORE", "DSEL_CALL_SPARSE_ATTN", "DSEL_F16", "DSEL_E4M3"):
+        assert getattr(T, name) == header_define(name)
