@@ -155,7 +155,7 @@ def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repe
         raise ValueError("out must be a contiguous float32 tensor [rows, n], n >= vocab a multiple of 16")
 
     def call(handle):
-        o = out if out is not None else logits.new_empty((rows, vocab + 15 & ~15), dtype=_F32)
+        o = out if out is not None else logits.new_empty(rows, vocab + 15 & ~15, dtype=_F32)
         status = _call(DSEL_CALL_LOGITS, _LOGITS.pack(
             logits.data_ptr(), dt, rows, vocab, x_stride, p_tokens, t_dt, width, t_stride, p_prompt, p_total, p_rep,
             p_freq, p_pres, p_boff, p_bids, p_bval, n_bias, p_mask, m_stride, m_count, p_mrows, o.data_ptr(),
@@ -179,25 +179,28 @@ def _operand_dtype(name, t, byte):
 
 
 def _queries(q, table, end, seq_ids):
-    """Checks what every query of a paged cache comes with: (device, tokens, table stride, address of end, of seq_ids)."""
-    dev = q.get_device()
-    if dev < 0 or q.dim() != 3:
+    """Checks what every query of a paged cache comes with.
+
+    Returns the device, q's shape and strides, the table's shape and row stride, the addresses of end and seq_ids."""
+    dev, q_shape = q.get_device(), q.shape
+    if dev < 0 or len(q_shape) != 3:
         raise ValueError("q must be a 3-D CUDA tensor [tokens, heads, dim] (there is no CPU path)")
-    tokens = q.shape[0]
-    if q.stride(2) != 1:
+    q_stride, tokens = q.stride(), q_shape[0]
+    if q_stride[2] != 1:
         raise ValueError("q must be contiguous in its last dimension")
     if table.dtype is not _I32:
         raise TypeError("block_table must be int32")
     t_stride = _rows_of("block_table", table, dev, None)
+    t_shape = table.shape
     if end is None:
         raise ValueError("end (the keys each query sees) must be given")
     p_end = _vector("end", end, dev, _I32, tokens)
     p_seq = 0
     if seq_ids is not None:
         p_seq = _vector("seq_ids", seq_ids, dev, _I32, tokens)
-    elif table.shape[0] != 1 and table.shape[0] != tokens:
+    elif t_shape[0] != 1 and t_shape[0] != tokens:
         raise ValueError("block_table needs one row, or one for each query, or seq_ids=")
-    return dev, tokens, t_stride, p_end, p_seq
+    return dev, q_shape, q_stride, t_shape, t_stride, p_end, p_seq
 
 
 def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=None, row_stride=None, out_dtype=None,
@@ -216,15 +219,15 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
     TopK row-stride requirement.  ``out`` may supply that tensor.
     """
     dt = _operand_dtype("q", q, True)
-    dev, tokens, t_stride, p_end, p_seq = _queries(q, block_table, end, seq_ids)
-    _, heads, dim = q.shape
-    if (keys.dtype is not q.dtype or keys.get_device() != dev or keys.dim() != 3 or keys.shape[2] != dim
-            or keys.stride(2) != 1):
+    dev, (tokens, heads, dim), (q_token, q_head, _), (seqs, t_width), t_stride, p_end, p_seq = _queries(
+        q, block_table, end, seq_ids)
+    k_shape = keys.shape
+    if keys.dtype is not q.dtype or keys.get_device() != dev or len(k_shape) != 3 or k_shape[2] != dim or keys.stride()[2] != 1:
         raise ValueError("keys must be [pages, page_size, dim] of q's type on its device, contiguous in the last dimension")
     if weights.dtype is not _F32 or weights.shape != (tokens, heads):
         raise ValueError("weights must be float32 [tokens, heads]")
     w_stride = _rows_of("weights", weights, dev, tokens)
-    pages, page, _ = keys.shape
+    pages, page, _ = k_shape
     k_page, k_row, _ = keys.stride()
     p_scale = s_stride = 0
     if key_scale is not None:
@@ -232,7 +235,6 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
             raise ValueError("key_scale must be float32 [pages, page_size]")
         s_stride = _rows_of("key_scale", key_scale, dev, pages)
         p_scale = key_scale.data_ptr()
-    seqs, t_width = block_table.shape
     if out is not None:
         if out.dim() != 2 or out.get_device() != dev or out.shape[0] != tokens or not out.is_contiguous():
             raise ValueError("out must be a contiguous tensor [tokens, row_stride]")
@@ -248,8 +250,7 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
         raise TypeError("scores are bfloat16 or float32")
 
     def call(handle):
-        o = out if out is not None else weights.new_empty((tokens, row_stride), dtype=out_dtype)
-        q_token, q_head, _ = q.stride()
+        o = out if out is not None else weights.new_empty(tokens, row_stride, dtype=out_dtype)
         status = _call(DSEL_CALL_INDEX_SCORE, _SCORE.pack(
             q.data_ptr(), dt, tokens, heads, dim, q_token, q_head, weights.data_ptr(), w_stride, keys.data_ptr(),
             pages, page, k_page, k_row, p_scale, s_stride, block_table.data_ptr(), seqs, t_width, t_stride, p_seq,
@@ -277,8 +278,8 @@ def sparse_attention(q, k_cache, v_cache, block_table, indices, end, *, block=1,
     float32 logarithms of the sums of exponentials [tokens, q_heads].
     """
     dt = _operand_dtype("q", q, False)
-    dev, tokens, t_stride, p_end, p_seq = _queries(q, block_table, end, seq_ids)
-    _, heads, dim = q.shape
+    dev, (tokens, heads, dim), (q_token, q_head, _), (seqs, t_width), t_stride, p_end, p_seq = _queries(
+        q, block_table, end, seq_ids)
     shape = k_cache.shape
     if len(shape) != 4 or shape[3] != dim or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [pages, page_size, kv_heads, dim], dim that of q")
@@ -306,10 +307,8 @@ def sparse_attention(q, k_cache, v_cache, block_table, indices, end, *, block=1,
         raise ValueError("out must be a contiguous tensor of q's shape and type")
 
     def call(handle):
-        o = out if out is not None else q.new_empty((tokens, heads, dim))
-        lse = q.new_empty((tokens, heads), dtype=_F32) if return_lse else None
-        q_token, q_head, _ = q.stride()
-        seqs, t_width = block_table.shape
+        o = out if out is not None else q.new_empty(tokens, heads, dim)
+        lse = q.new_empty(tokens, heads, dtype=_F32) if return_lse else None
         status = _call(DSEL_CALL_SPARSE_ATTN, _ATTN.pack(
             q.data_ptr(), dt, tokens, heads, kv_heads, dim, q_token, q_head, k_cache.data_ptr(), v_cache.data_ptr(),
             pages, page, k_page, k_row, k_head, v_page, v_row, v_head, block_table.data_ptr(), seqs, t_width,
