@@ -17,6 +17,7 @@ plain, and the arguments go to the library packed into one array (``dsel_call``)
 """
 from __future__ import annotations
 
+import contextlib
 import struct
 
 import torch
@@ -36,15 +37,15 @@ _I32, _I64, _F32, _BF16, _F16, _E4M3 = (torch.int32, torch.int64, torch.float32,
                                         torch.float8_e4m3fn)
 
 
-def _run(device, stream, call):
-    """``call(stream handle)`` with CUDA device `device` current and, for a given stream, as torch's current one."""
-    if stream is None and _current_device() == device:
-        return call(_stream_of(device))
+@contextlib.contextmanager
+def _on(device, stream):
+    """CUDA device `device` as the current one and, where a raw stream handle is given, that stream as torch's."""
     with torch.cuda.device(device):
         if stream is None:
-            return call(_stream_of(device))
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-            return call(stream)
+            yield
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+                yield
 
 
 def _vector(name, t, device, dtype, count):
@@ -101,6 +102,11 @@ def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repe
     dev = logits.get_device()
     if dev < 0 or logits.dim() != 2:
         raise ValueError("logits must be a 2-D CUDA tensor [rows, vocab] (there is no CPU path)")
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return process_logits(logits, tokens=tokens, prompt_len=prompt_len, total_len=total_len, repetition=repetition,
+                                  frequency=frequency, presence=presence, bias_offsets=bias_offsets, bias_ids=bias_ids,
+                                  bias_values=bias_values, mask=mask, mask_rows=mask_rows, out=out)
     if logits.dtype is _BF16:
         dt = DSEL_BF16
     elif logits.dtype is _F32:
@@ -154,17 +160,14 @@ def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repe
                             or out.shape[1] < vocab or out.shape[1] % 16 or not out.is_contiguous()):
         raise ValueError("out must be a contiguous float32 tensor [rows, n], n >= vocab a multiple of 16")
 
-    def call(handle):
-        o = out if out is not None else logits.new_empty(rows, vocab + 15 & ~15, dtype=_F32)
-        status = _call(DSEL_CALL_LOGITS, _LOGITS.pack(
-            logits.data_ptr(), dt, rows, vocab, x_stride, p_tokens, t_dt, width, t_stride, p_prompt, p_total, p_rep,
-            p_freq, p_pres, p_boff, p_bids, p_bval, n_bias, p_mask, m_stride, m_count, p_mrows, o.data_ptr(),
-            o.shape[1], handle))
-        if status != DSEL_OK:
-            raise DselError(status)
-        return o
-
-    return _run(dev, stream, call)
+    o = out if out is not None else logits.new_empty(rows, vocab + 15 & ~15, dtype=_F32)
+    status = _call(DSEL_CALL_LOGITS, _LOGITS.pack(
+        logits.data_ptr(), dt, rows, vocab, x_stride, p_tokens, t_dt, width, t_stride, p_prompt, p_total, p_rep,
+        p_freq, p_pres, p_boff, p_bids, p_bval, n_bias, p_mask, m_stride, m_count, p_mrows, o.data_ptr(),
+        o.shape[1], _stream_of(dev)))
+    if status != DSEL_OK:
+        raise DselError(status)
+    return o
 
 
 def _operand_dtype(name, t, byte):
@@ -221,6 +224,10 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
     dt = _operand_dtype("q", q, True)
     dev, (tokens, heads, dim), (q_token, q_head, _), (seqs, t_width), t_stride, p_end, p_seq = _queries(
         q, block_table, end, seq_ids)
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return index_score(q, weights, keys, block_table, end, seq_ids=seq_ids, key_scale=key_scale,
+                               row_stride=row_stride, out_dtype=out_dtype, out=out)
     k_shape = keys.shape
     if keys.dtype is not q.dtype or keys.get_device() != dev or len(k_shape) != 3 or k_shape[2] != dim or keys.stride()[2] != 1:
         raise ValueError("keys must be [pages, page_size, dim] of q's type on its device, contiguous in the last dimension")
@@ -249,17 +256,14 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
     if out_dtype is not _BF16 and out_dtype is not _F32:
         raise TypeError("scores are bfloat16 or float32")
 
-    def call(handle):
-        o = out if out is not None else weights.new_empty(tokens, row_stride, dtype=out_dtype)
-        status = _call(DSEL_CALL_INDEX_SCORE, _SCORE.pack(
-            q.data_ptr(), dt, tokens, heads, dim, q_token, q_head, weights.data_ptr(), w_stride, keys.data_ptr(),
-            pages, page, k_page, k_row, p_scale, s_stride, block_table.data_ptr(), seqs, t_width, t_stride, p_seq,
-            p_end, o.data_ptr(), DSEL_F32 if out_dtype is _F32 else DSEL_BF16, row_stride, handle))
-        if status != DSEL_OK:
-            raise DselError(status)
-        return o
-
-    return _run(dev, stream, call)
+    o = out if out is not None else weights.new_empty(tokens, row_stride, dtype=out_dtype)
+    status = _call(DSEL_CALL_INDEX_SCORE, _SCORE.pack(
+        q.data_ptr(), dt, tokens, heads, dim, q_token, q_head, weights.data_ptr(), w_stride, keys.data_ptr(),
+        pages, page, k_page, k_row, p_scale, s_stride, block_table.data_ptr(), seqs, t_width, t_stride, p_seq,
+        p_end, o.data_ptr(), DSEL_F32 if out_dtype is _F32 else DSEL_BF16, row_stride, _stream_of(dev)))
+    if status != DSEL_OK:
+        raise DselError(status)
+    return o
 
 
 def sparse_attention(q, k_cache, v_cache, block_table, indices, end, *, block=1, seq_ids=None, scale=None, out=None,
@@ -280,6 +284,10 @@ def sparse_attention(q, k_cache, v_cache, block_table, indices, end, *, block=1,
     dt = _operand_dtype("q", q, False)
     dev, (tokens, heads, dim), (q_token, q_head, _), (seqs, t_width), t_stride, p_end, p_seq = _queries(
         q, block_table, end, seq_ids)
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return sparse_attention(q, k_cache, v_cache, block_table, indices, end, block=block, seq_ids=seq_ids,
+                                    scale=scale, out=out, return_lse=return_lse)
     shape = k_cache.shape
     if len(shape) != 4 or shape[3] != dim or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [pages, page_size, kv_heads, dim], dim that of q")
@@ -306,17 +314,14 @@ def sparse_attention(q, k_cache, v_cache, block_table, indices, end, *, block=1,
                             or not out.is_contiguous()):
         raise ValueError("out must be a contiguous tensor of q's shape and type")
 
-    def call(handle):
-        o = out if out is not None else q.new_empty(tokens, heads, dim)
-        lse = q.new_empty(tokens, heads, dtype=_F32) if return_lse else None
-        status = _call(DSEL_CALL_SPARSE_ATTN, _ATTN.pack(
-            q.data_ptr(), dt, tokens, heads, kv_heads, dim, q_token, q_head, k_cache.data_ptr(), v_cache.data_ptr(),
-            pages, page, k_page, k_row, k_head, v_page, v_row, v_head, block_table.data_ptr(), seqs, t_width,
-            t_stride, p_seq, p_end, indices.data_ptr(), i_dt, take, i_stride[0],
-            i_stride[1] if len(i_shape) == 3 else 0, block, scale, o.data_ptr(),
-            0 if lse is None else lse.data_ptr(), handle))
-        if status != DSEL_OK:
-            raise DselError(status)
-        return (o, lse) if return_lse else o
-
-    return _run(dev, stream, call)
+    o = out if out is not None else q.new_empty(tokens, heads, dim)
+    lse = q.new_empty(tokens, heads, dtype=_F32) if return_lse else None
+    status = _call(DSEL_CALL_SPARSE_ATTN, _ATTN.pack(
+        q.data_ptr(), dt, tokens, heads, kv_heads, dim, q_token, q_head, k_cache.data_ptr(), v_cache.data_ptr(),
+        pages, page, k_page, k_row, k_head, v_page, v_row, v_head, block_table.data_ptr(), seqs, t_width,
+        t_stride, p_seq, p_end, indices.data_ptr(), i_dt, take, i_stride[0],
+        i_stride[1] if len(i_shape) == 3 else 0, block, scale, o.data_ptr(),
+        0 if lse is None else lse.data_ptr(), _stream_of(dev)))
+    if status != DSEL_OK:
+        raise DselError(status)
+    return (o, lse) if return_lse else o
