@@ -13,8 +13,15 @@
 // counted into shared memory (one 32-bit word per vocabulary entry of the slice:
 // integer atomics, so the result does not depend on their order), and one pass
 // over the registers applies everything and writes the row.  Every CTA of a row
-// scans the row's tokens itself: they come from L2, and a scan costs two
+// scans the row's tokens itself: they come from L2, and a scan costs a few
 // instructions per token against a second launch and a count array in HBM.
+//
+// Measured (one B200, 256 rows of 129,280 f32, up to 16,384 tokens each): 95.5 us, of which
+// the stream alone takes 42.1 (the copy rate), the mask 3, the biases 7, the scans 18 and
+// the entries they met 17 to 25: bound by instructions (64% of issue slots busy).  Tried and
+// dropped: penalties written sparsely after a pure stream (134 us: each phase waits for
+// the one before), prompt and answer in two branch-free scans (117 us), a warp of its own
+// for the biases (102 us).
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -25,6 +32,8 @@
 namespace dsel {
 namespace {
 
+// 256 threads: with 512 (slices of 8,192, half the scans) 256 rows take 90.4 us, but 64 rows 20.5 against 19.4
+// and one row 3.7 against 3.3.
 constexpr int kLgThreads = 256;
 constexpr int kLgVecs = 4;                            // vectors of 4 elements each thread holds
 constexpr int kLgSlice = kLgThreads * kLgVecs * 4;    // vocabulary entries of a CTA

@@ -20,6 +20,11 @@
 // issues the products.  Pages of a power of two of at least 8 keys are boxes of a
 // tensor map; pages of other sizes end anywhere in a tile, so there two warps address
 // each key by itself and copy it in 16-byte pieces.
+//
+// Measured (one B200, 64 heads of 128): 64 queries over 64 K to 128 K keys each, bf16
+// 255 us (1,637 MB, 0.98 of the copy rate), e4m3 with scales 167 us (852 MB, 0.78: the
+// accumulators' round trip through barriers takes as long as a 16 KB tile); 1,024 queries
+// over 65,536 keys 850 to 970 us with the power limit (1,091 GFLOP, 1,130 to 1,280 TFLOP/s).
 #include <cstdint>
 
 #include <cuda.h>
