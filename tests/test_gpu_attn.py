@@ -82,6 +82,26 @@ def test_many_units_and_splits():
         check(run(a, b), a, b)
 
 
+def test_one_long_list():
+    # 131,072 positions of one query: the running sums of every group over many tiles
+    a, b = make(31, hq=4, dim=64, page=64, width=2100, block=64, take=2048, ends=[130_001])
+    a["indices"][0] = torch.randperm(2100)[:2048].to(torch.int32)
+    check(run(a, b), a, b)
+
+
+def test_rising_scores():
+    # every tile's scores lie above the last one's: the reference moves again and again, or not by enough to
+    n = 1024
+    for dim, factor in ((64, 0.02), (128, 0.4)):
+        a, b = make(32, hq=20, dim=dim, take=n, page=64, width=16, ends=[n])
+        a["indices"][0] = torch.arange(n)
+        row = a["block_table"][0].long()
+        ramp = (torch.arange(n) * factor).view(16, 64, 1, 1)
+        a["k_cache"][row] = (a["k_cache"][row].float() * 0.1 + ramp / dim ** 0.5).to(torch.bfloat16)
+        a["q"][:] = 1.0
+        check(run(a, b), a, b)
+
+
 def test_nothing_to_read():
     a, b = make(1, tokens=6, hq=5, take=33, ends=[0, -3, 256, 256, 256, 1])
     a["indices"][2] = -1

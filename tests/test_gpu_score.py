@@ -68,6 +68,21 @@ def test_chunks_of_queries(heads, tokens):
     check(run(a, out_dtype=torch.float32), a)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "e4m3"])
+@pytest.mark.parametrize("heads,dim", [(5, 128), (16, 32), (64, 128), (90, 64)])
+@pytest.mark.parametrize("tokens,page", [(3, 64), (21, 16), (21, 24)])
+def test_chunks_of_other_types(dtype, heads, dim, tokens, page):
+    width = -(-700 // page)
+    ends = [max(0, 700 - 30 * i) for i in range(tokens)]
+    a = make(tokens + heads, tokens=tokens, heads=heads, dim=dim, page=page, width=width, dtype=dtype, scale=True, ends=ends)
+    check(run(a, out_dtype=torch.float32), a)
+
+
+def test_one_long_context():
+    a = make(30, heads=4, dim=32, page=64, width=5000, ends=[319_950])
+    check(run(a), a)
+
+
 @pytest.mark.parametrize("page", [1, 7, 16, 33, 64, 128, 200, 1000])
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_page_sizes(page, dtype):
