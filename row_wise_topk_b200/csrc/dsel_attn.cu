@@ -41,6 +41,7 @@ constexpr int kAtThreads = kAtWarps * 32;
 // warps fit an SM (with tiles of 32 four did, and a 1,024-query chunk took 443 us); groups of two and
 // four warps share theirs.
 constexpr int at_tile(int row_warps) { return row_warps == 1 ? 16 : 32; }
+constexpr int kAtSm = 228 * 1024;   // shared memory of an SM
 constexpr int kAtMaxStages = 3;
 constexpr int kAtMaxCluster = 8;
 constexpr int kPitchPad = 8;       // floats: rows of the partial sums fall on different banks
@@ -126,9 +127,9 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float peer_load(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float2 peer_load2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ float4 peer_load4(uint32_t addr) {
@@ -497,29 +498,39 @@ __global__ void __launch_bounds__(kAtThreads, kRowWarps == 1 ? 3 : 1) attn_kerne
     }
     return;
   }
-  const int parts = int(ranks) * kGroups;
-  float* total = wt + parts * kRows;
+  // Remote loads are issued four at a time: one takes as long as the four.
+  const int parts = int(ranks) * kGroups;                             // at least 2, a power of two
+  float* sums = wt + parts * kRows;                                   // [parts][kRows] sums, then [kRows] totals
+  float* total = sums + parts * kRows;
   if (int(threadIdx.x) < kRows) {
     const int r = int(threadIdx.x);
-    float top = -__int_as_float(0x7F800000);
-    for (int i = 0; i < parts; ++i) {
-      const float mi = peer_load(peer_addr(shared_addr(ml + ((i % kGroups) * kRows + r) * 2), uint32_t(i / kGroups)));
-      wt[i * kRows + r] = mi;
-      top = fmaxf(top, mi);
+    float top = kNone;
+    for (int i = 0; i < parts; i += 4) {
+      float2 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = i + j < parts ? i + j : parts - 1;
+        x[j] = peer_load2(peer_addr(shared_addr(ml + ((k % kGroups) * kRows + r) * 2), uint32_t(k / kGroups)));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = i + j < parts ? i + j : parts - 1;
+        wt[k * kRows + r] = x[j].x;
+        sums[k * kRows + r] = x[j].y;
+        top = fmaxf(top, x[j].x);
+      }
     }
-    const float z = top == -__int_as_float(0x7F800000) ? 0.f : top;
+    const float z = top == kNone ? 0.f : top;
     float sum = 0.f;
     for (int i = 0; i < parts; ++i) {
-      const float li = peer_load(peer_addr(shared_addr(ml + ((i % kGroups) * kRows + r) * 2 + 1), uint32_t(i / kGroups)));
-      const float w = pow2((wt[i * kRows + r] - z) * p.scale_log2);
-      wt[i * kRows + r] = w;
-      sum += li * w;
+      const float f = pow2((wt[i * kRows + r] - z) * p.scale_log2);
+      wt[i * kRows + r] = f;
+      sum += sums[i * kRows + r] * f;
     }
     total[r] = sum;
     const int head = rt * kRows + r;
     if (rank == 0 && p.lse != nullptr && head < p.group)
-      p.lse[out0 + head] =
-          sum == 0.f ? -__int_as_float(0x7F800000) : (z * p.scale_log2 + log2f(sum)) * 0.6931471805599453f;
+      p.lse[out0 + head] = sum == 0.f ? kNone : (z * p.scale_log2 + log2f(sum)) * 0.6931471805599453f;
   }
   __syncthreads();
   for (int i = int(rank) * kAtThreads + int(threadIdx.x); i < kRows * kDim / 4; i += int(ranks) * kAtThreads) {
@@ -527,19 +538,29 @@ __global__ void __launch_bounds__(kAtThreads, kRowWarps == 1 ? 3 : 1) attn_kerne
     const int head = rt * kRows + r;
     if (head >= p.group) continue;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < parts; ++j) {
-      const float w = wt[j * kRows + r];
-      const float4 b = peer_load4(peer_addr(shared_addr(part + ((j % kGroups) * kRows + r) * kPitch + c), uint32_t(j / kGroups)));
-      a.x += b.x * w;
-      a.y += b.y * w;
-      a.z += b.z * w;
-      a.w += b.w * w;
+    const uint32_t here_at = shared_addr(part + r * kPitch + c);
+    for (int j = 0; j < parts; j += 4) {
+      float4 x[4];
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        const int k = j + q4 < parts ? j + q4 : parts - 1;
+        x[q4] = peer_load4(peer_addr(here_at, uint32_t(k / kGroups)) + uint32_t((k % kGroups) * kRows * kPitch * 4));
+      }
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        if (j + q4 < parts) {
+          const float f = wt[(j + q4) * kRows + r];
+          a.x += x[q4].x * f;
+          a.y += x[q4].y * f;
+          a.z += x[q4].z * f;
+          a.w += x[q4].w * f;
+        }
+      }
     }
     const float sum = total[r];
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const uint2 y = make_uint2(pack16<kBf16>(a.x * inv, a.y * inv), pack16<kBf16>(a.z * inv, a.w * inv));
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) +
-                              ((out0 + head) * kDim + c) * 2) = y;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + ((out0 + head) * kDim + c) * 2) = y;
   }
   cluster_sync_all();   // no CTA leaves while a peer may still read its sums
 }
@@ -559,11 +580,14 @@ int launch_attn(AttnParams p, int64_t units, int dev, int sms, cudaStream_t st) 
   // CTAs of single-warp groups share an SM (1,024-query chunk 309 -> 244 us; 256 CTAs at once 51 -> 54 us).
   const int most = kRowWarps == 1 && units * cluster > 2 * int64_t(sms) ? 2 : kAtMaxStages;
   p.stages = each < 1 ? 1 : (each > most ? most : int(each));
-  const int merge = kAtWarps * 16 * (kDim + kPitchPad + 2) * 4 + (cluster * kGroups + 1) * 16 * kRowWarps * 4;
-  const int smem = p.stages * kStageBytes > merge ? p.stages * kStageBytes : merge;
+  const int merge = kAtWarps * 16 * (kDim + kPitchPad + 2) * 4 + (2 * cluster * kGroups + 1) * 16 * kRowWarps * 4;
+  int smem = p.stages * kStageBytes > merge ? p.stages * kStageBytes : merge;
+  // Few CTAs are spread over the SMs by asking for so much that no SM takes more than its share (64 queries x 512
+  // keys of 64 heads, clusters of four: 14.0 us, and 17.2 where three CTAs fit an SM and clusters crowd some).
+  const int64_t share = (units * cluster + sms - 1) / sms;
+  if (share <= 2 && smem < kAtSm / int(share + 1) + 1024) smem = kAtSm / int(share + 1) + 1024;
   if (units * cluster > INT32_MAX) return DSEL_ERR_ROWS;
-  if (allow_smem(reinterpret_cast<const void*>(kern), kAtMaxStages * kStageBytes > 64 * 1024 ? kAtMaxStages * kStageBytes : 64 * 1024,
-                 dev, &allowed) != cudaSuccess)
+  if (allow_smem(reinterpret_cast<const void*>(kern), kAtSm / 2 + 1024, dev, &allowed) != cudaSuccess)
     return DSEL_ERR_CUDA;
   return launch_dependent(kern, unsigned(units * cluster), kAtThreads, cluster, uint32_t(smem), st, p) == cudaSuccess
              ? DSEL_OK
