@@ -21,7 +21,8 @@
 // the entries they met 17 to 25: bound by instructions (64% of issue slots busy).  Tried and
 // dropped: penalties written sparsely after a pure stream (134 us: each phase waits for
 // the one before), prompt and answer in two branch-free scans (117 us), a warp of its own
-// for the biases (102 us).
+// for the biases (102 us), scans shared in clusters of eight through distributed shared memory
+// (126 us).
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -291,8 +292,8 @@ DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, 
                          int64_t mask_count, const int32_t* mask_rows, float* out, int64_t out_stride, void* stream) {
   if (dtype != DSEL_BF16 && dtype != DSEL_F32) return DSEL_ERR_DTYPE;
   if (rows < 0) return DSEL_ERR_ROWS;
-  if (vocab < 1 || vocab > INT32_MAX - 2 * kLgSlice) return DSEL_ERR_SHAPE;
-  if (x_stride < vocab || out_stride < vocab || out_stride % kStrideReq != 0 || out_stride > INT32_MAX - kLgSlice)
+  if (vocab < 1 || vocab > INT32_MAX - 16 * kLgSlice) return DSEL_ERR_SHAPE;
+  if (x_stride < vocab || out_stride < vocab || out_stride % kStrideReq != 0 || out_stride > INT32_MAX - 16 * kLgSlice)
     return DSEL_ERR_STRIDE;
   if (tokens != nullptr) {
     if (token_dtype != DSEL_I32 && token_dtype != DSEL_I64) return DSEL_ERR_INDEX_DTYPE;

@@ -90,6 +90,29 @@ def test_long_history_many_repeats_int64():
     check(run(a), a)
 
 
+@pytest.mark.parametrize("ids", [torch.int32, torch.int64])
+@pytest.mark.parametrize("rows,vocab,shift", [(40, 70001, 3), (150, 20000, 0), (75, 33000, 1)])
+def test_long_texts_of_a_batch(ids, rows, vocab, shift):
+    # batches that fill the GPU, texts of thousands of tokens with many repeats, at any alignment
+    a = make(rows + shift, rows, vocab, width=2500, ids=ids, masked=True, biases=20, spread=vocab // 3)
+    toks = torch.full((rows, 2500 + shift), 5, dtype=ids, device="cuda")[:, shift:]
+    toks.copy_(a["tokens"])
+    a["repetition"][1], a["frequency"][1], a["presence"][1] = 1.0, 0.0, 0.0       # its tokens are not read
+    a["total_len"][2] = 0
+    d = {k: v.cuda() for k, v in a.items() if k not in ("x", "tokens")}
+    x = a["x"].cuda()
+    got = T.process_logits(x, tokens=toks, **d)
+    want = torch.stack([T.process_logits(x[r:r + 1], tokens=toks[r:r + 1], **{k: v[r:r + 1] for k, v in d.items()
+                                         if k in ("total_len", "prompt_len", "repetition", "frequency", "presence", "mask_rows")},
+                                         mask=d["mask"], bias_offsets=d["bias_offsets"][r:r + 2], bias_ids=d["bias_ids"],
+                                         bias_values=d["bias_values"])[0] for r in range(rows)])
+    assert torch.equal(got, want)              # a row by itself (the other launch shape) gives the same bits
+    few = {k: (v[:3] if k in ("x", "tokens", "total_len", "prompt_len", "repetition", "frequency", "presence", "mask_rows") else v)
+           for k, v in a.items()}
+    few["bias_offsets"] = a["bias_offsets"][:4]
+    check(got[:3], few)
+
+
 def test_lengths_out_of_range_are_clamped():
     a = make(3, 4, 500, width=64)
     a["total_len"] = torch.tensor([-5, 1000, 64, 0], dtype=torch.int32)
