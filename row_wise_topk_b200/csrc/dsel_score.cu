@@ -22,9 +22,9 @@
 // each key by itself and copy it in 16-byte pieces.
 //
 // Measured (one B200, 64 heads of 128): 64 queries over 64 K to 128 K keys each, bf16
-// 255 us (1,637 MB, 0.98 of the copy rate), e4m3 with scales 167 us (852 MB, 0.78: the
-// accumulators' round trip through barriers takes as long as a 16 KB tile); 1,024 queries
-// over 65,536 keys 850 to 970 us with the power limit (1,091 GFLOP, 1,130 to 1,280 TFLOP/s).
+// 255 us (1,637 MB, 0.98 of the copy rate), e4m3 with scales 140 us (852 MB, 0.93); 1,024
+// queries over 65,536 keys 830 to 970 us with the power limit (1,091 GFLOP, 1,120 to 1,310
+// TFLOP/s).
 #include <cstdint>
 
 #include <cuda.h>
@@ -76,6 +76,7 @@ struct ScoreParams {
   int32_t ring, lag;                      // key tiles in shared memory; copied tiles in flight before the oldest is awaited
   int32_t q_bufs;                         // query buffers
   int32_t chunk;                          // key tiles per work item
+  int32_t balanced;                       // shares instead of ranges (see Walk)
   int32_t chunks, items;
   int32_t seq_mode;                       // 0: seq_ids, 1: token t is sequence t, 2: one sequence
   int32_t out_f32;
@@ -217,7 +218,7 @@ struct Item {
   int32_t token0, count;   // queries of the item
   int32_t seq, end;        // this lane's query: its sequence (-1: none) and its visible keys
   uint32_t starts;         // bit i: lane i starts a run
-  int32_t tile0;           // first key tile
+  int32_t tile0, limit;           // first key tile
 };
 
 // Stores y as float32 or bfloat16 where `on`, without a branch: the code around it stays one block.
@@ -242,26 +243,83 @@ struct Cursor {
   }
 };
 
+// Key tiles that query t sees.
+__device__ __forceinline__ int32_t tiles_of(const ScoreParams& p, int32_t t) {
+  const int32_t seq = p.seq_mode == 0 ? p.seq_ids[t] : (p.seq_mode == 1 ? t : 0);
+  const int32_t end = p.end[t];
+  if (seq < 0 || seq >= p.seqs || end < 0) return 0;
+  return int32_t(((end > p.row_stride ? p.row_stride : int64_t(end)) + kTile - 1) / kTile);
+}
+
+// The work of a CTA, item by item: which queries, and from which of their key tiles on.
+//   dealt:    ranges of `chunk` tiles of every query group, one grid apart;
+//   balanced: an equal share of all queries' tiles, one after another, found by summing what each query sees
+//             (one query an item).
+struct Walk {
+  int32_t item, group, tile0;
+  int32_t left;   // balanced: tiles left of the share
+  __device__ __forceinline__ bool more(const ScoreParams& p) const {
+    return p.balanced ? left > 0 && group < p.tokens : item < p.items;
+  }
+};
+__device__ __forceinline__ void deal(const ScoreParams& p, Walk& w, int32_t item) {
+  w.item = item;
+  w.group = item / p.chunks;
+  w.tile0 = (item - w.group * p.chunks) * p.chunk;
+}
+__device__ __forceinline__ Walk first_walk(const ScoreParams& p) {
+  Walk w = {0, 0, 0, 0};
+  if (!p.balanced) {
+    deal(p, w, int32_t(blockIdx.x));
+    return w;
+  }
+  const int lane = int(threadIdx.x & 31);
+  const int32_t each = (p.tokens + 31) / 32, t0 = lane * each;   // queries of a lane
+  int64_t mine = 0;
+  for (int32_t j = 0; j < each; ++j) mine += t0 + j < p.tokens ? tiles_of(p, t0 + j) : 0;
+  int64_t upto = mine;   // tiles of this lane's queries and all before
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += v;
+  }
+  const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  const int64_t from = total * blockIdx.x / gridDim.x, to = total * (blockIdx.x + 1) / gridDim.x;
+  if (from >= to) return w;
+  const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, upto > from)) - 1;
+  int64_t at = __shfl_sync(0xFFFFFFFFu, upto - mine, owner);   // tiles before the owner's queries
+  w.group = owner * each;
+  for (;;) {   // (ends: the owner's queries reach past `from`)
+    const int32_t n = tiles_of(p, w.group);
+    if (at + n > from) break;
+    at += n;
+    ++w.group;
+  }
+  w.tile0 = int32_t(from - at);
+  w.left = int32_t(to - from);
+  return w;
+}
+
 // What the queries of an item come with, read an item ahead of its use.
 struct ItemRead {
   int32_t seq, end;
 };
-__device__ __forceinline__ ItemRead read_item(const ScoreParams& p, int32_t item, int per_item) {
+__device__ __forceinline__ ItemRead read_item(const ScoreParams& p, const Walk& w, int per_item) {
   ItemRead r = {-1, 0};
   const int lane = int(threadIdx.x & 31);
-  const int64_t t = int64_t(item / p.chunks) * per_item + lane;
-  if (item < p.items && lane < per_item && t < p.tokens) {
+  const int64_t t = int64_t(w.group) * per_item + lane;
+  if (w.more(p) && lane < per_item && t < p.tokens) {
     r.seq = p.seq_mode == 0 ? p.seq_ids[t] : (p.seq_mode == 1 ? int32_t(t) : 0);
     r.end = p.end[t];
   }
   return r;
 }
-__device__ __forceinline__ Item make_item(const ScoreParams& p, int32_t item, int per_item, const ItemRead& r) {
+__device__ __forceinline__ Item make_item(const ScoreParams& p, const Walk& w, int per_item, const ItemRead& r) {
   Item it;
   const int lane = int(threadIdx.x & 31);
-  const int32_t group = item / p.chunks;
-  it.tile0 = (item - group * p.chunks) * p.chunk;
-  it.token0 = group * per_item;
+  it.tile0 = w.tile0;
+  it.limit = p.balanced ? w.left : p.chunk;
+  it.token0 = w.group * per_item;
   it.count = p.tokens - it.token0 < per_item ? p.tokens - it.token0 : per_item;
   it.seq = r.seq < 0 || r.seq >= p.seqs ? -1 : r.seq;
   it.end = r.end < 0 || it.seq < 0 ? 0 : (r.end > p.row_stride ? int32_t(p.row_stride) : r.end);
@@ -285,8 +343,19 @@ __device__ __forceinline__ Run load_run(const ScoreParams& p, const Item& it, in
   r.seq = __shfl_sync(0xFFFFFFFFu, it.seq, a);
   r.end = __reduce_max_sync(0xFFFFFFFFu, lane >= a && lane < r.b ? it.end : 0);
   const int32_t n = (r.end + kTile - 1) / kTile - it.tile0;
-  r.tiles = n < 0 ? 0 : (n > p.chunk ? p.chunk : n);
+  r.tiles = n < 0 ? 0 : (n > it.limit ? it.limit : n);
   return r;
+}
+
+// To the next item; the one that ends is `it`.
+__device__ __forceinline__ void step_walk(const ScoreParams& p, Walk& w, const Item& it) {
+  if (p.balanced) {
+    w.left -= load_run(p, it, 0).tiles;
+    ++w.group;
+    w.tile0 = 0;
+  } else {
+    deal(p, w, w.item + int32_t(gridDim.x));
+  }
 }
 
 // Where a key lies: its page as the table gives it (-1: none), and its place in the page.
@@ -378,10 +447,30 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     uint32_t parity = 0;  // bit a: accumulator a's next fill
     uint32_t turn = 0;    // key tiles so far (col_tiles == 1: accumulators take turns)
     bool ok = true;
-    ItemRead ahead = read_item(p, int32_t(blockIdx.x), per_item);
-    for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
-      const Item it = make_item(p, item, per_item, ahead);
-      ahead = read_item(p, item + int32_t(gridDim.x), per_item);
+    // -inf from column `from` to `to` (multiples of 16) of a query's row: both warpgroups' threads, 16 bytes each
+    auto fill = [&](int32_t token, int64_t from, int64_t to) {
+      const int step = p.out_f32 ? 4 : 8;
+      const uint32_t none = p.out_f32 ? 0xFF800000u : 0xFF80FF80u;
+      for (int64_t pos = from + int64_t(threadIdx.x) * step; pos < to; pos += kEpiWarps * 32 * step) {
+        const int64_t o = (int64_t(token) * p.row_stride + pos) * (p.out_f32 ? 4 : 2);
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + o) = make_uint4(none, none, none, none);
+      }
+    };
+    if (p.balanced) {   // what no query sees, in pieces, while the first tiles are on their way
+      constexpr int64_t kPieceCols = 8192;
+      const int64_t pieces = (p.row_stride + kPieceCols - 1) / kPieceCols;
+      for (int64_t u = blockIdx.x; u < pieces * p.tokens; u += gridDim.x) {
+        const int32_t token = int32_t(u / pieces);
+        const int64_t col = u % pieces * kPieceCols, seen = int64_t(tiles_of(p, token)) * kTile;
+        fill(token, seen > col ? seen : col, col + kPieceCols < p.row_stride ? col + kPieceCols : p.row_stride);
+      }
+    }
+    Walk walk = first_walk(p);
+    ItemRead ahead = read_item(p, walk, per_item);
+    while (walk.more(p) && ok) {
+      const Item it = make_item(p, walk, per_item, ahead);
+      step_walk(p, walk, it);
+      ahead = read_item(p, walk, per_item);
       // the weights of this thread's columns
       float w[kSets][kMyCols / 4];
 #pragma unroll
@@ -523,15 +612,9 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
         }
         finish();
         last.hi = 0;
-        // -inf behind the run's last tile (both warpgroups' threads, 16 bytes each)
-        const int64_t from = pos0 + int64_t(run.tiles) * kTile;
-        const int step = p.out_f32 ? 4 : 8;
-        const uint32_t fill = p.out_f32 ? 0xFF800000u : 0xFF80FF80u;
-        for (int qi = run.a; qi < run.b; ++qi)
-          for (int64_t pos = from + int64_t(threadIdx.x) * step; pos < pos_end; pos += kEpiWarps * 32 * step) {
-            const int64_t o = (int64_t(it.token0 + qi) * p.row_stride + pos) * (p.out_f32 ? 4 : 2);
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + o) = make_uint4(fill, fill, fill, fill);
-          }
+        // -inf behind the run's last tile
+        if (!p.balanced)
+          for (int qi = run.a; qi < run.b; ++qi) fill(it.token0 + qi, pos0 + int64_t(run.tiles) * kTile, pos_end);
       }
     }
   } else if (warp < kEpiWarps + kProdWarps) {
@@ -576,10 +659,12 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
         uint32_t turn = 0;
         const int boxes = kTile / p.box_keys, per_batch = 32 / boxes;
         const uint32_t box_bytes = uint32_t(p.box_keys) * 128u;
-        ItemRead ahead = read_item(p, int32_t(blockIdx.x), per_item);
-        for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
-          const Item it = make_item(p, item, per_item, ahead);
-          ahead = read_item(p, item + int32_t(gridDim.x), per_item);
+        Walk walk = first_walk(p);
+        ItemRead ahead = read_item(p, walk, per_item);
+        while (walk.more(p) && ok) {
+          const Item it = make_item(p, walk, per_item, ahead);
+          step_walk(p, walk, it);
+          ahead = read_item(p, walk, per_item);
           bool queries = false;   // loaded for this item
           for (int a = 0; a < it.count && ok;) {
             const Run run = load_run(p, it, a);
@@ -636,10 +721,12 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
       }
     } else {
       const int per_row = p.row_bytes / 16;   // 16-byte pieces of a key
-      ItemRead ahead = read_item(p, int32_t(blockIdx.x), per_item);
-      for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
-        const Item it = make_item(p, item, per_item, ahead);
-        ahead = read_item(p, item + int32_t(gridDim.x), per_item);
+      Walk walk = first_walk(p);
+      ItemRead ahead = read_item(p, walk, per_item);
+      while (walk.more(p) && ok) {
+        const Item it = make_item(p, walk, per_item, ahead);
+        step_walk(p, walk, it);
+        ahead = read_item(p, walk, per_item);
         bool queries = false;   // loaded for this item
         for (int a = 0; a < it.count && ok;) {
           const Run run = load_run(p, it, a);
@@ -708,10 +795,12 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
     bool ok = mw == 0 || !kShare;
     const int steps = p.row_bytes / 32;
     const uint64_t key_operand = operand(ring0), q_operand = operand(q0);
-    ItemRead ahead = read_item(p, int32_t(blockIdx.x), per_item);
-    for (int32_t item = int32_t(blockIdx.x); item < p.items && ok; item += int32_t(gridDim.x)) {
-      const Item it = make_item(p, item, per_item, ahead);
-      ahead = read_item(p, item + int32_t(gridDim.x), per_item);
+    Walk walk = first_walk(p);
+    ItemRead ahead = read_item(p, walk, per_item);
+    while (walk.more(p) && ok) {
+      const Item it = make_item(p, walk, per_item, ahead);
+      step_walk(p, walk, it);
+      ahead = read_item(p, walk, per_item);
       bool any = false;
       for (int a = 0; a < it.count && ok;) {
         const Run run = load_run(p, it, a);
@@ -969,7 +1058,13 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
   if (best < 0) return DSEL_ERR_ROWS;
   p.chunks = int32_t((tiles + p.chunk - 1) / p.chunk);
   p.items = int32_t(groups * p.chunks);
-  const int grid = p.items < sms ? p.items : sms;
+  // A query an item, not too many of them to sum on the way in: every CTA takes the same number of tiles in one go,
+  // however ragged the sequences.  (Ranges of 16 tiles dealt out: e4m3 decoding 167 us, an item's start costs four of
+  // its tiles; ranges of 32: the same, and bf16 262 us for 255, since some CTAs got one more than others.)
+  // Where every tile has a CTA of its own, the sum would only come before it (1 x 8,192: 5.7 us for 4.8).
+  const int64_t most_tiles = tokens * tiles;
+  p.balanced = !wide && tokens <= 1024 && most_tiles > sms;
+  const int grid = p.balanced ? int(most_tiles < sms ? most_tiles : sms) : (p.items < sms ? p.items : sms);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return dtype == DSEL_E4M3 ? launch_type<true>(p, dtype, hp, wide, grid, smem, dev, cs)
                             : launch_type<false>(p, dtype, hp, wide, grid, smem, dev, cs);
