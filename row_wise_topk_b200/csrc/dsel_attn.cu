@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kAtThreads, kRowWarps == 1 ? 3 : 1) attn_kerne
       at = locate(p, table, pos_next);
       pos_next = entry(i + kBatch);
       exist = __ballot_sync(0xFFFFFFFFu, at.page >= 0);
-      slot = at.page >= 0 ? at.page * p.page_size + at.row : -1;   // (used where it fits)
+      slot = at.page >= 0 && p.rows_even ? at.page * p.page_size + at.row : -1;
     }
     const uint32_t any = (exist >> (sub * kAtTile)) & kFullTile;
     if (any == 0u) return 0u;

@@ -135,11 +135,12 @@ def test_long_rows_many_items():
     check(run(a), a)
 
 
+@pytest.mark.parametrize("n", [149, 700, 1300])
 @pytest.mark.parametrize("page", [16, 20])
 @pytest.mark.parametrize("heads", [8, 64])
-def test_many_short_sequences(page, heads):
-    # several work items for each CTA, rows of zero to six tiles in no order, a scale for each key
-    n = 700
+def test_many_short_sequences(page, heads, n):
+    # several work items for each CTA (equal shares, and from 1,025 queries on ranges), rows of zero to six tiles in
+    # no order, a scale for each key
     ends = [(i * 37) % 730 if i % 5 else (i * 64) % 390 for i in range(n)]
     a = make(page + heads, seqs=n, tokens=n, heads=heads, dim=32, page=page, width=-(-736 // page), dtype="e4m3", scale=True,
              ends=ends)
@@ -238,6 +239,21 @@ def test_topk_takes_the_rows():
         if n > 64:
             assert torch.equal(idx[r], with_end[1][r]) and int(idx[r].max()) < n
         assert torch.equal(with_end[0][r][: len(want)].float().sort(descending=True).values, want)
+
+
+def test_most_queries_see_nothing():
+    # shares that begin and end anywhere, long stretches without a key, an unknown sequence between
+    n = 600
+    ends = [0] * n
+    for i, e in ((3, 5000), (4, 128), (300, 1), (301, 4999), (599, 257)):
+        ends[i] = e
+    ids = list(range(n))
+    ids[301], ids[5] = -1, n
+    a = make(33, seqs=n, tokens=n, heads=16, dim=32, page=64, width=79, ends=ends, ids=ids)
+    check(run(a), a)
+    a["end"][:] = 0
+    got = run(a)
+    assert (got == float("-inf")).all()
 
 
 def test_no_tokens():
