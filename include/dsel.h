@@ -363,7 +363,9 @@ DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, 
  * belongs to sequence seq_ids[t] and sees the keys before end[t]; a seq_ids[t]
  * outside [0, seqs) leaves it none.  seq_ids NULL: query t is of sequence t
  * (tokens == seqs), or all are of the only one (seqs == 1).  Queries of one sequence
- * are served fastest next to each other; any order is right.
+ * are served fastest next to each other; any order is right.  dsel_index_score goes
+ * by tokens / seqs whether it has one query for each sequence or a chunk of them: a
+ * table of the call's sequences alone serves a chunk faster than one with rows to spare.
  */
 
 /*
@@ -375,7 +377,8 @@ DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, 
  * in float32, rounded once to out_dtype; a NaN in q or a key gives a NaN score.
  * A "key" is whatever is to be selected: a token's, or one that stands for a block.
  *   q            device [tokens][heads][dim] of `dtype` (DSEL_BF16 / _F16 / _E4M3), strides
- *                in elements; dim a multiple of 32 from 32 to 128, heads 1 to 128
+ *                in elements (queries may not overlap); dim a multiple of 32 from 32 to
+ *                128, heads 1 to 128
  *   weights      device float32 [tokens][heads], row stride weights_stride
  *   keys         device [pages][page_size][dim] of `dtype`, strides in elements (page_size
  *                any); base, row and page strides of q and keys multiples of 16 bytes

@@ -15,11 +15,11 @@
 // heads costs 1.5 instructions per (key, head): the epilogue of one accumulator runs
 // under the products of the other.
 //
-// Roles of a persistent CTA: 8 warps read accumulators, sum over heads and store
-// (warpgroup b owns accumulator b), one warp brings key tiles and queries by TMA, one
-// issues the products.  Pages of a power of two of at least 8 keys are boxes of a
-// tensor map; pages of other sizes end anywhere in a tile, so there two warps address
-// each key by itself and copy it in 16-byte pieces.
+// Roles of a persistent CTA: 8 warps read accumulators, sum over heads and store; two
+// bring key tiles (and one of them the queries) by TMA; one, in decoding two, issue the
+// products.  Pages of a power of two of at least 8 keys are boxes of a tensor map; pages
+// of other sizes end anywhere in a tile, so there the two warps address each key by
+// itself and copy it in 16-byte pieces.
 //
 // Measured (one B200, 64 heads of 128): 64 queries over 64 K to 128 K keys each, bf16
 // 255 us (1,637 MB, 0.98 of the copy rate), e4m3 with scales 140 us (852 MB, 0.93); 1,024

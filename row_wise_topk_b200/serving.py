@@ -213,8 +213,8 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
     ``q``: [tokens, heads, dim], bfloat16, float16 or float8_e4m3fn.  ``weights``: float32
     [tokens, heads].  ``keys``: [pages, page_size, dim] of q's type, ``key_scale`` float32
     [pages, page_size] or None.  ``block_table``: int32 [sequences, width], the pages of each
-    sequence in order.  ``end``: int32 [tokens], the keys each query sees (the ``end`` of
-    ``topk``).  ``seq_ids``: int32 [tokens], each query's sequence; None: query t is of
+    sequence in order (best of this call's sequences alone).  ``end``: int32 [tokens], the keys
+    each query sees (the ``end`` of ``topk``).  ``seq_ids``: int32 [tokens], each query's sequence; None: query t is of
     sequence t, or all are of the only one.
 
     Returns [tokens, row_stride] in ``out_dtype`` (bfloat16, or float32), -inf where a query
