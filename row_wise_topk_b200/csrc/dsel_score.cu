@@ -720,7 +720,8 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
         }
       }
     } else {
-      const int per_row = p.row_bytes / 16;   // 16-byte pieces of a key
+      const int per_row = p.row_bytes / 16;   // 16-byte pieces of a key: 2, 4, 6, 8, 12 or 16
+      const int inverse = (65536 + per_row - 1) / per_row;   // i * inverse / 65536 is i / per_row for every piece of a tile
       Walk walk = first_walk(p);
       ItemRead ahead = read_item(p, walk, per_item);
       while (walk.more(p) && ok) {
@@ -761,8 +762,9 @@ __global__ void __launch_bounds__(kScThreads, 1) score_kernel(const __grid_const
                                      : -1;
             const uint32_t dst0 = ring0 + slot * stage_bytes + uint32_t(pw) * (kProdKeys * 128);
             // consecutive lanes bring consecutive pieces
+#pragma unroll 4
             for (int i = lane; i < kProdKeys * per_row; i += 32) {
-              const int r = i / per_row, piece = i - r * per_row;
+              const int r = (i * inverse) >> 16, piece = i - r * per_row;
               const int64_t o0 = __shfl_sync(0xFFFFFFFFu, off0, r & 31), o1 = __shfl_sync(0xFFFFFFFFu, off1, r & 31);
               const int64_t o = r < 32 ? o0 : o1;
               copy16(dst0 + uint32_t(piece >> 3) * kPanel + uint32_t(r) * 128u + (uint32_t((piece ^ r) & 7) << 4),
