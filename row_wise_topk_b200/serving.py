@@ -44,7 +44,9 @@ def _on(device, stream):
         if stream is None:
             yield
         else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+            # (0 is the default stream's handle, but no external stream: torch would take one of its own pool for it)
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream != 0
+                                   else torch.cuda.default_stream(device)):
                 yield
 
 

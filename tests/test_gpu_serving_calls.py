@@ -172,3 +172,35 @@ def test_two_captured_steps_replay_in_any_order():
         torch.cuda.synchronize()
         for (_, f), o in zip(runs, outs):
             assert all(torch.equal(x, y) for x, y in zip(f(), o))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", ["logits", "attention", "score"])
+def test_the_default_streams_handle(op):
+    """stream=0 is what current_stream().cuda_stream gives outside every stream context: the default stream
+    itself, behind the work that is on it."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    table = torch.arange(20, device="cuda", dtype=torch.int32).view(4, 5)
+    end = torch.full((4,), 80, device="cuda", dtype=torch.int32)
+    if op == "logits":
+        x = r(4, 1000)
+        f = lambda **kw: T.process_logits(x, **kw)
+    elif op == "attention":
+        x, c = r(4, 8, 64).bfloat16(), r(20, 16, 2, 64).bfloat16()
+        idx = torch.arange(60, device="cuda", dtype=torch.int32).repeat(4, 1)
+        f = lambda **kw: T.sparse_attention(x, c, c, table, idx, end, **kw)
+    else:
+        x, w, keys = r(4, 16, 64).bfloat16(), r(4, 16), r(20, 16, 64).bfloat16()
+        f = lambda **kw: T.index_score(x, w, keys, table, end, **kw)
+    want, final = f(), x.clone()
+    out = torch.zeros_like(want)    # (an allocation might wait for the device, and so might making streams)
+    torch.cuda.Stream()
+    handle = torch.cuda.current_stream().cuda_stream
+    assert handle == 0
+    x.zero_()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(1 << 26)      # tens of ms
+    x.copy_(final)
+    got = f(stream=handle, out=out)
+    assert torch.equal(got, want)
