@@ -500,7 +500,8 @@ DSEL_API int dsel_plan_device(int dtype, int64_t rows, int64_t row_stride, int32
                               dsel_plan_t* out);
 
 /* Reads and clears the device-side status word that kernels set when a bounded
- * wait runs out (it should never happen).  Synchronises `stream`.  *status_out
+ * wait runs out (it should never happen; the launch then ends without all of its
+ * outputs written).  Synchronises `stream`.  *status_out
  * receives 0 or DSEL_ERR_DEVICE_TIMEOUT.  Returns DSEL_OK or DSEL_ERR_CUDA. */
 DSEL_API int dsel_device_status(int* status_out, void* stream);
 

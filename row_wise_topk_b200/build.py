@@ -13,7 +13,8 @@ LIB = os.path.join(HERE, "libdsel.so")
 STATS_LIB = os.path.join(HERE, "libdsel_stats.so")   # same library, with per-CTA counters
 SOURCES = ["dsel_api.cu", "dsel_plan.cpp", "dsel_shard.cu", "dsel_logits.cu", "dsel_score.cu",
            "dsel_attn.cu", "dsel_call.cpp"]
-HEADERS = ["dsel_device.cuh", "dsel_kernels.cuh", "dsel_ops.cuh", "dsel_plan.h", "dsel_resident.cuh", "dsel_slice.cuh"]
+HEADERS = ["dsel_device.cuh", "dsel_kernels.cuh", "dsel_ops.cuh", "dsel_plan.h", "dsel_resident.cuh", "dsel_slice.cuh",
+           "dsel_wait.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -32,6 +32,7 @@
 #include <cuda_runtime.h>
 
 #include "dsel_ops.cuh"
+#include "dsel_wait.cuh"
 
 namespace dsel {
 
@@ -83,41 +84,8 @@ struct ScoreParams {
 };
 
 // ---- PTX ----
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0u;
-}
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-// Bounded wait: false (and a device status) after two seconds.
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = now_ns();
-  while (!bar_try(bar, parity)) {
-    if (now_ns() - t0 > kWaitLimit) {
-      atomicExch(&g_score_status, DSEL_ERR_DEVICE_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-  return bar_try(bar, parity) || bar_wait_slow(bar, parity);
+  return warp_wait(bar, parity, kWaitLimit, &g_score_status);
 }
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
