@@ -409,7 +409,8 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
  * i of query t's list that lie before end[t] and exist (above).  Indices below 0
  * (dsel_topk's sentinels) are skipped; an index that is listed twice counts twice.
  * Query head h reads key head h / (q_heads / kv_heads).  Products and sums in
- * float32, the probabilities rounded to `dtype` for the product with v, o rounded
+ * float32, the probabilities rounded to `dtype` for the product with v (in float16
+ * as multiples of 2^-11, so that terms down to 2^-36 of the largest count), o rounded
  * once.  A query with nothing to read, or only scores of -inf, gets o = 0 and
  * lse = -inf; what lies in keys and values that it does not read has no effect.
  *   q            device [tokens][q_heads][dim] of `dtype` (DSEL_BF16 / _F16), strides in

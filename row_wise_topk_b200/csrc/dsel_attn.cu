@@ -17,7 +17,9 @@
 // has 16 to 64 rows and its operands arrive row by row in any order.
 //
 // Probabilities are rounded to the operands' type for the product with v (the matrix
-// instruction takes both of one type); their sum is kept of the float32 values.
+// instruction takes both of one type); their sum is kept of the float32 values.  float16
+// ends at 2^-25, so there they are taken 2^11 times as large: else the terms of a long list
+// far below its largest score would be in the sum and not in the product.
 //
 // Measured (one B200): 64 queries of 32 heads over 4, 32 blocks of 64 positions each 47 us
 // (269 MB, 0.87 of the copy rate); 1,024 queries of one sequence over 16 such blocks
@@ -193,6 +195,10 @@ __global__ void __launch_bounds__(kAtThreads, kRowWarps == 1 ? 3 : 1) attn_kerne
   constexpr int kAtTile = at_tile(kRowWarps);
   constexpr int kTileBytes = kAtTile * kRowBytes;        // keys of a tile; its values follow
   constexpr int kPitch = kDim + kPitchPad;
+  // How far (in powers of two) a score may lie above its row's reference, and what a probability of 1 is in the
+  // product with v.  In float16 both together stay below 2^16: terms down to 2^-36 count, each within 2^-36.
+  constexpr float kAhead = kBf16 ? 8.f : 4.f;
+  constexpr float kUnit = kBf16 ? 1.f : 2048.f;
   const int warp = int(threadIdx.x >> 5), lane = int(threadIdx.x & 31);
   const int grp = warp / kRowWarps, rw = warp % kRowWarps;
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
@@ -389,10 +395,10 @@ __global__ void __launch_bounds__(kAtThreads, kRowWarps == 1 ? 3 : 1) attn_kerne
       x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
       x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 2));
       x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 2));
-      // The reference m of a row moves only where a score is 2^8 above it: terms and sums then are at most that much
-      // larger, which no type here minds, and the sums of nearly every tile need no new factor (with a move for
+      // The reference m of a row moves only where a score is 2^kAhead above it: terms and sums then are at most that
+      // much larger, which no type here minds, and the sums of nearly every tile need no new factor (with a move for
       // every new maximum some row of a warp had one in most tiles).
-      const bool up0 = (x0 - m0) * p.scale_log2 > 8.f, up1 = (x1 - m1) * p.scale_log2 > 8.f;
+      const bool up0 = (x0 - m0) * p.scale_log2 > kAhead, up1 = (x1 - m1) * p.scale_log2 > kAhead;
       if (__any_sync(0xFFFFFFFFu, up0 || up1)) {
         // (a row without a score so far has m = -inf and holds zeros)
         const float f0 = up0 ? pow2((m0 - x0) * p.scale_log2) : 1.f, f1 = up1 ? pow2((m1 - x1) * p.scale_log2) : 1.f;
@@ -421,9 +427,10 @@ __global__ void __launch_bounds__(kAtThreads, kRowWarps == 1 ? 3 : 1) attn_kerne
       }
 #pragma unroll
       for (int n = 0; n < kAtTile / 16; ++n) {
-        const uint32_t a[4] = {pack16<kBf16>(s[2 * n][0], s[2 * n][1]), pack16<kBf16>(s[2 * n][2], s[2 * n][3]),
-                               pack16<kBf16>(s[2 * n + 1][0], s[2 * n + 1][1]),
-                               pack16<kBf16>(s[2 * n + 1][2], s[2 * n + 1][3])};
+        const uint32_t a[4] = {pack16<kBf16>(s[2 * n][0] * kUnit, s[2 * n][1] * kUnit),
+                               pack16<kBf16>(s[2 * n][2] * kUnit, s[2 * n][3] * kUnit),
+                               pack16<kBf16>(s[2 * n + 1][0] * kUnit, s[2 * n + 1][1] * kUnit),
+                               pack16<kBf16>(s[2 * n + 1][2] * kUnit, s[2 * n + 1][3] * kUnit)};
 #pragma unroll
         for (int d = 0; d < kDim / 16; ++d) {
           uint32_t b[4];
@@ -490,7 +497,7 @@ __global__ void __launch_bounds__(kAtThreads, kRowWarps == 1 ? 3 : 1) attn_kerne
         a.z += b.z * f;
         a.w += b.w * f;
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float inv = sum == 0.f ? 0.f : (1.f / kUnit) / sum;
       const uint2 y = make_uint2(pack16<kBf16>(a.x * inv, a.y * inv), pack16<kBf16>(a.z * inv, a.w * inv));
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + ((out0 + head) * kDim + c) * 2) = y;
       if (c == 0 && p.lse != nullptr)
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(kAtThreads, kRowWarps == 1 ? 3 : 1) attn_kerne
       }
     }
     const float sum = total[r];
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : (1.f / kUnit) / sum;
     const uint2 y = make_uint2(pack16<kBf16>(a.x * inv, a.y * inv), pack16<kBf16>(a.z * inv, a.w * inv));
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + ((out0 + head) * kDim + c) * 2) = y;
   }

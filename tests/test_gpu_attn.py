@@ -287,3 +287,30 @@ def test_serving_step(tokens, k, block):
     assert np.all(off <= rounds[fine] * 2.0 ** -24 * mag[fine])
     token, prob = T.topk_sample(y, 1, torch.zeros(n, device="cuda"))
     assert torch.equal(token, y.argmax(1)) and (prob == 1).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,dim", [(4, 64), (20, 128), (64, 64)])
+@pytest.mark.parametrize("far", [0, 17_000, 32_767])
+def test_one_score_far_above_a_long_flat_list(dtype, hq, dim, far):
+    """Terms e^-18 of the largest each, 32,768 of them: they are all of the result where the largest one's value
+    is 0.
+
+    Tolerance: the oracle's bound, and where terms are too small for float16's relative rounding (2^-25 at most
+    of what a term of the reference is, 2^11 there): 2^-36 of the largest term for each, times its value."""
+    n = 32768
+    a, b = make(far + hq, hq=hq, dim=dim, dtype=dtype, page=64, width=n // 64, block=64, take=n // 64, ends=[n])
+    a["indices"][0] = torch.arange(n // 64)
+    row = a["block_table"][0].long()
+    a["q"][:] = 1.0
+    a["k_cache"][:] = 0.0
+    a["v_cache"][:] = a["v_cache"].abs()
+    a["k_cache"][row[far // 64], far % 64] = 18 / dim ** 0.5
+    a["v_cache"][row[far // 64], far % 64] = 0.0
+    o, lse = run(a, b)
+    k = {name: t.double().numpy() if t.is_floating_point() else t.numpy() for name, t in a.items()}
+    want = S.oracle_attention(k["q"], k["k_cache"], k["v_cache"], k["block_table"], k["indices"], k["end"], block=b,
+                              eps=EPS[a["q"].dtype])
+    small = np.abs(k["v_cache"][row.numpy()]).sum(axis=(0, 1))[0] * (2.0 ** -36 if dtype == "f16" else 0.0)
+    assert np.all(np.abs(o.cpu().double().numpy() - want[0]) <= want[2] + small)
+    assert np.all(np.abs(lse.cpu().double().numpy() - want[1]) <= want[3])
