@@ -343,7 +343,8 @@ DSEL_API int dsel_take_index(const int64_t* table, int64_t table_stride, const v
  *                masked), or row r where mask_rows is NULL.  mask NULL: none.
  *   out          device float32 [rows][out_stride], 16-byte aligned; out_stride >= vocab, a
  *                multiple of dsel_stride_requirement(DSEL_F32).  May be x itself
- *                (DSEL_F32, the same stride); other overlaps return DSEL_ERR_OVERLAP.
+ *                (DSEL_F32, the same stride or one row); other overlaps return
+ *                DSEL_ERR_OVERLAP.
  * Returns DSEL_OK, DSEL_ERR_DTYPE / _ROWS / _SHAPE / _STRIDE / _INDEX_DTYPE / _NULL /
  * _ALIGN / _OVERLAP / _DEVICE or DSEL_ERR_CUDA.  One launch, asynchronous on
  * `stream`, no workspace; can be captured.

@@ -316,7 +316,7 @@ DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, 
   if (rows > INT32_MAX / slices) return DSEL_ERR_ROWS;
   // in place only where every element is read and written by one thread
   if (ranges_meet(x, (rows - 1) * x_stride + vocab, eb, out, rows * out_stride, 4) &&
-      !(x == out && dtype == DSEL_F32 && x_stride == out_stride))
+      !(x == out && dtype == DSEL_F32 && (x_stride == out_stride || rows == 1)))   // (one row: no stride counts)
     return DSEL_ERR_OVERLAP;
   LogitsParams p = {};
   p.slices = slices;

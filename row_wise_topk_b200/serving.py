@@ -99,7 +99,8 @@ def process_logits(logits, *, tokens=None, prompt_len=None, total_len=None, repe
 
     Returns float32 [rows, n], n = vocab rounded up to the TopK row-stride requirement,
     with -inf in the columns behind the vocabulary.  ``out`` may supply that tensor; it
-    may be ``logits`` itself when that is float32, contiguous and of such a width.
+    may be ``logits`` itself when that is float32, contiguous and of such a width, or the
+    buffer of such a width whose first ``vocab`` columns ``logits`` is.
     """
     dev = logits.get_device()
     if dev < 0 or logits.dim() != 2:

@@ -246,3 +246,15 @@ def test_sampler_draws_from_processed_rows():
 
 def test_no_rows():
     assert T.process_logits(torch.zeros(0, 10, device="cuda")).shape == (0, 16)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 5])
+@pytest.mark.parametrize("vocab", [1000, 1003, 1008])
+def test_in_place_in_a_padded_buffer(rows, vocab):
+    # logits are the first columns of the buffer that is written: any number of rows, one as well
+    a = make(rows + vocab, rows, vocab, width=50, biases=9, masked=True)
+    d = {k: v.cuda() for k, v in a.items()}
+    buf = torch.full((rows, 1024), 7.0, device="cuda")
+    buf[:, :vocab] = d.pop("x")
+    assert T.process_logits(buf[:, :vocab], out=buf, **d) is buf
+    check(buf, a)
