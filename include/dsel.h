@@ -360,7 +360,9 @@ DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, 
  * Paged caches (dsel_index_score, dsel_sparse_attn).  Key s of sequence b lies in
  * page table[b][s / page_size], at place s % page_size in it.  A key whose place in
  * the table is outside it (s / page_size >= table_width) or whose page is outside
- * [0, pages) does not exist: it scores -inf and takes no part in attention.  Query t
+ * [0, pages) does not exist: it scores -inf and takes no part in attention.  Where
+ * pages, seqs or table_width is 0 there are none, and table, keys, k and v may be
+ * NULL.  Query t
  * belongs to sequence seq_ids[t] and sees the keys before end[t]; a seq_ids[t]
  * outside [0, seqs) leaves it none.  seq_ids NULL: query t is of sequence t
  * (tokens == seqs), or all are of the only one (seqs == 1).  Queries of one sequence
@@ -411,7 +413,7 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
  * (dsel_topk's sentinels) are skipped; an index that is listed twice counts twice.
  * Query head h reads key head h / (q_heads / kv_heads).  Products and sums in
  * float32, the probabilities rounded to `dtype` for the product with v (in float16
- * as multiples of 2^-11, so that terms down to 2^-36 of the largest count), o rounded
+ * 2^11 times as large, so that terms down to 2^-36 of the largest count), o rounded
  * once.  A query with nothing to read, or only scores of -inf, gets o = 0 and
  * lse = -inf; what lies in keys and values that it does not read has no effect.
  *   q            device [tokens][q_heads][dim] of `dtype` (DSEL_BF16 / _F16), strides in

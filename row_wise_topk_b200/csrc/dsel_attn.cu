@@ -646,8 +646,10 @@ DSEL_API int dsel_sparse_attn(const void* q, int dtype, int64_t tokens, int32_t 
         v_head_stride) & 7) != 0)
     return DSEL_ERR_STRIDE;   // rows are copied in 16-byte pieces
   if (tokens == 0) return DSEL_OK;
-  if (q == nullptr || k == nullptr || v == nullptr || table == nullptr || end == nullptr || out == nullptr ||
-      (indices == nullptr && take > 0))
+  // A cache without pages, or a table without places, has no positions: no query is of any sequence, and neither is read.
+  const bool no_keys = pages == 0 || seqs == 0 || table_width == 0;
+  if (q == nullptr || end == nullptr || out == nullptr || (indices == nullptr && take > 0) ||
+      (!no_keys && (k == nullptr || v == nullptr || table == nullptr)))
     return DSEL_ERR_NULL;
   if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
         reinterpret_cast<uintptr_t>(out)) & 15u) != 0)
@@ -686,7 +688,7 @@ DSEL_API int dsel_sparse_attn(const void* q, int dtype, int64_t tokens, int32_t 
   p.pages = pages;
   p.page_size = page_size;
   p.page_shift = log2_of(page_size);
-  p.seqs = seqs;
+  p.seqs = no_keys ? 0 : seqs;
   p.table_width = table_width;
   p.seq_mode = seq_ids != nullptr ? 0 : (seqs == 1 ? 2 : 1);
   p.kv_heads = kv_heads;

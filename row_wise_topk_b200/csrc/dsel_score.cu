@@ -948,7 +948,10 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
       page_stride * eb % 16 != 0)
     return DSEL_ERR_STRIDE;
   if (tokens == 0) return DSEL_OK;
-  if (q == nullptr || weights == nullptr || keys == nullptr || table == nullptr || end == nullptr || out == nullptr)
+  // A cache without pages, or a table without places, has no keys: no query is of any sequence, and neither is read.
+  const bool no_keys = pages == 0 || seqs == 0 || table_width == 0;
+  if (q == nullptr || weights == nullptr || end == nullptr || out == nullptr ||
+      (!no_keys && (keys == nullptr || table == nullptr)))
     return DSEL_ERR_NULL;
   if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(keys) | reinterpret_cast<uintptr_t>(out)) & 15u) != 0)
     return DSEL_ERR_ALIGN;
@@ -974,7 +977,7 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
   p.page_shift = -1;
   for (int s = 0; s < 31; ++s)
     if ((int64_t(1) << s) == page_size) p.page_shift = s;
-  p.seqs = seqs;
+  p.seqs = no_keys ? 0 : seqs;
   p.table_width = table_width;
   p.tokens = int32_t(tokens);
   p.heads = heads;
@@ -1004,7 +1007,7 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
   const int64_t q_head = heads > 1 ? q_head_stride * eb : p.row_bytes;
   const int64_t q_token = tokens > 1 ? q_token_stride * eb : heads * q_head;
   if (!encode(&p.q_map, dtype, q, dim, heads, tokens, q_head, q_token, inner, hp, cols / hp)) return DSEL_ERR_STRIDE;
-  p.box_keys = p.page_shift >= 3 && pages > 0 ? (page_size < kTile ? page_size : kTile) : 0;
+  p.box_keys = p.page_shift >= 3 && !no_keys ? (page_size < kTile ? page_size : kTile) : 0;
   if (p.box_keys > 0 && !encode(&p.key_map, dtype, keys, dim, page_size, pages, p.key_bytes,
                                 pages > 1 ? p.page_bytes : int64_t(page_size) * p.key_bytes, inner, p.box_keys, 1))
     p.box_keys = 0;

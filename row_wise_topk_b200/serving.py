@@ -253,7 +253,7 @@ def index_score(q, weights, keys, block_table, end, *, seq_ids=None, key_scale=N
         row_stride, out_dtype = out.shape[1], out.dtype
     else:
         if row_stride is None:
-            row_stride = t_width * page + 15 & ~15
+            row_stride = max(t_width * page + 15 & ~15, 16)   # (a row of the TopK has some columns)
         if out_dtype is None:
             out_dtype = _BF16
     if out_dtype is not _BF16 and out_dtype is not _F32:

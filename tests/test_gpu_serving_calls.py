@@ -204,3 +204,26 @@ def test_the_default_streams_handle(op):
     x.copy_(final)
     got = f(stream=handle, out=out)
     assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,seqs", [(1, 1), (4, 4), (4, 0), (40, 1), (300, 300)])
+@pytest.mark.parametrize("pages,width,page", [(0, 3, 16), (0, 0, 16), (6, 0, 16), (0, 3, 10), (6, 0, 10)])
+def test_caches_without_keys(tokens, seqs, pages, width, page):
+    """A cache before its first page, or a table without places: scores of -inf, attention over nothing."""
+    table, end = i32(seqs, width), i32(tokens) + 20
+    ids = i32(tokens) if seqs == 0 else None
+    q = torch.randn(tokens, 8, 64, device="cuda").bfloat16()
+    for out_dtype in (torch.bfloat16, torch.float32):
+        rows = T.index_score(q, torch.randn(tokens, 8, device="cuda"), q.new_empty(pages, page, 64), table, end, seq_ids=ids,
+                             key_scale=torch.empty(pages, page, device="cuda"), out_dtype=out_dtype)
+        assert rows.shape == (tokens, max(16, -(-width * page // 16) * 16)) and (rows == float("-inf")).all()
+    wide = T.index_score(q, torch.randn(tokens, 8, device="cuda"), q.new_empty(pages, page, 64), table, end, seq_ids=ids,
+                         row_stride=20000)
+    assert wide.shape == (tokens, 20000) and (wide == float("-inf")).all()
+    for idx in (i32(tokens, 9), i32(tokens, 2, 9).long(), i32(tokens, 0)):
+        for block in (1, 3, 16):
+            c = q.new_empty(pages, page, 2, 64)
+            o, lse = T.sparse_attention(q, c, c, table, idx, end, block=block, seq_ids=ids, return_lse=True)
+            assert (o == 0).all() and (lse == float("-inf")).all()
+    assert T.dsel_device_status() == 0

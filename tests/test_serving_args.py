@@ -160,3 +160,12 @@ def test_packed_calls():
     assert T.lib.dsel_call(3, words) == header_define("DSEL_ERR_UNAVAILABLE")
     for name in ("DSEL_CALL_LOGITS", "DSEL_CALL_INDEX_SCORE", "DSEL_CALL_SPARSE_ATTN", "DSEL_F16", "DSEL_E4M3"):
         assert getattr(T, name) == header_define(name)
+
+
+@pytest.mark.parametrize("pages,width", [(1, 5), (10, 1)])
+def test_caches_may_be_null_only_where_there_are_no_keys(pages, width):
+    null = header_define("DSEL_ERR_NULL")
+    for name in ("keys", "table"):
+        assert score(**{name: None, "pages": pages, "table_width": width}) == null
+    for name in ("k", "v", "table"):
+        assert attn(**{name: None, "pages": pages, "table_width": width}) == null
