@@ -261,3 +261,14 @@ def test_no_tokens():
     d = {k: v.cuda() for k, v in a.items()}
     got = T.index_score(d["q"][:0], d["weights"][:0], d["keys"], d["block_table"], d["end"][:0])
     assert got.shape == (0, 128)
+
+
+@pytest.mark.parametrize("tokens,rows", [(40, 40), (40, 64), (33, 500)])
+def test_a_chunk_against_a_table_with_spare_rows(tokens, rows):
+    # the host sees no more queries than table rows and takes the form for decoding; the scores are the same
+    a = make(tokens, tokens=tokens, heads=32, dim=64, page=16, width=20, ends=[320 - tokens + 1 + i for i in range(tokens)],
+             ids=[0] * tokens)
+    check(run(a, out_dtype=torch.float32), a)
+    b = dict(a, block_table=torch.full((rows, 20), -1, dtype=torch.int32), seq_ids=torch.full((tokens,), 7, dtype=torch.int32))
+    b["block_table"][7] = a["block_table"][0]
+    check(run(b, out_dtype=torch.float32), b)
