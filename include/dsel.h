@@ -368,7 +368,8 @@ DSEL_API int dsel_logits(const void* x, int dtype, int64_t rows, int32_t vocab, 
  * (tokens == seqs), or all are of the only one (seqs == 1).  Queries of one sequence
  * are served fastest next to each other; any order is right.  dsel_index_score goes
  * by tokens / seqs whether it has one query for each sequence or a chunk of them: a
- * table of the call's sequences alone serves a chunk faster than one with rows to spare.
+ * table of the call's sequences alone serves a chunk faster than one with rows to spare
+ * (512 queries of one sequence over 32,768 keys: 224 us, and 351 with a table of 1,024 rows).
  */
 
 /*
@@ -506,7 +507,9 @@ DSEL_API int dsel_plan_device(int dtype, int64_t rows, int64_t row_stride, int32
 /* Reads and clears the device-side status word that kernels set when a bounded
  * wait runs out (it should never happen; the launch then ends without all of its
  * outputs written).  Synchronises `stream`.  *status_out
- * receives 0 or DSEL_ERR_DEVICE_TIMEOUT.  Returns DSEL_OK or DSEL_ERR_CUDA. */
+ * receives 0 or DSEL_ERR_DEVICE_TIMEOUT (or DSEL_ERR_ALIGN, of a dsel_index_score
+ * launch whose shared memory was not placed as it must be: nothing was written).
+ * Returns DSEL_OK or DSEL_ERR_CUDA. */
 DSEL_API int dsel_device_status(int* status_out, void* stream);
 
 /* Per-CTA counters of the last streaming launch, for tuning.  Only builds made

@@ -22,9 +22,9 @@
 // far below its largest score would be in the sum and not in the product.
 //
 // Measured (one B200): 64 queries of 32 heads over 4, 32 blocks of 64 positions each 47 us
-// (269 MB, 0.87 of the copy rate); 1,024 queries of one sequence over 16 such blocks
-// 228 us (the 2.1 GB that they gather come out of L2 at 9.4 TB/s; 400 instructions a tile
-// of 16 bound it); 64 queries of 64 heads over one, 512 positions each 14.0 us (latency: the
+// (269 MB, 0.88 of the copy rate); 1,024 queries of one sequence over 16 such blocks
+// 230 us (the 2.1 GB that they gather come out of L2 at 9.3 TB/s; 400 instructions a tile
+// of 16 bound it); 64 queries of 64 heads over one, 512 positions each 13.6 us (latency: the
 // index, the page, the row, then the join, each a round trip).
 #include <cstdint>
 
@@ -39,9 +39,9 @@ namespace {
 
 constexpr int kAtWarps = 4;
 constexpr int kAtThreads = kAtWarps * 32;
-// Positions per tile.  A group of one warp owns a whole ring, so its tiles are small enough that eight
-// warps fit an SM (with tiles of 32 four did, and a 1,024-query chunk took 443 us); groups of two and
-// four warps share theirs.
+// Positions per tile.  A group of one warp owns a whole ring, so its tiles are small: the four rings of a CTA take
+// 96 KB with three stages (two CTAs an SM) and 64 KB with two (three CTAs); with tiles of 32 one CTA fitted,
+// and a 1,024-query chunk took 443 us.  Groups of two and four warps share theirs.
 constexpr int at_tile(int row_warps) { return row_warps == 1 ? 16 : 32; }
 constexpr int kAtSm = 228 * 1024;   // shared memory of an SM
 constexpr int kAtMaxStages = 3;

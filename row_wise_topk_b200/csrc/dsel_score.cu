@@ -22,9 +22,10 @@
 // itself and copy it in 16-byte pieces.
 //
 // Measured (one B200, 64 heads of 128): 64 queries over 64 K to 128 K keys each, bf16
-// 255 us (1,637 MB, 0.98 of the copy rate), e4m3 with scales 140 us (852 MB, 0.93); 1,024
-// queries over 65,536 keys 830 to 970 us with the power limit (1,091 GFLOP, 1,120 to 1,310
-// TFLOP/s).
+// 254 to 259 us (1,637 MB, 0.97 to 0.98 of the copy rate), e4m3 with scales 141 us in short
+// runs at full clocks to 173 us in long ones (852 MB, 0.92 to 0.75: a tile of 16 KB costs the same
+// barrier round trips as one of 32); 1,024 queries over 65,536 keys 890 to 990 us, in short and
+// long runs, with the power limit (1,091 GFLOP, 1,100 to 1,230 TFLOP/s).
 #include <cstdint>
 
 #include <cuda.h>
@@ -38,7 +39,7 @@ namespace dsel {
 
 namespace {
 
-__device__ int g_score_status;   // DSEL_ERR_DEVICE_TIMEOUT when a wait gave up
+__device__ int g_score_status;   // DSEL_ERR_DEVICE_TIMEOUT when a wait gave up, DSEL_ERR_ALIGN: shared memory unaligned
 
 constexpr int kTile = 128;            // keys per tile (TMEM lanes)
 constexpr int kPanel = kTile * 128;   // a tile's panel: 128 rows of 128 bytes, 128-byte swizzle
@@ -52,7 +53,7 @@ constexpr int kMaxAccs = 8;
 constexpr int kMaxRing = 8;
 constexpr int kScoreSmem = 227 * 1024;   // all of a CTA's shared memory
 constexpr int kBarBytes = 512;          // the barriers and the accumulators' address
-constexpr uint64_t kWaitLimit = 2000000000ull;   // 2 s
+constexpr uint64_t kWaitLimit = 2000000000ull;   // 2 s, in ns
 
 struct ScoreParams {
   CUtensorMap q_map;      // [tokens][heads][dim], boxes of one accumulator's queries, 128 bytes of depth
@@ -1033,11 +1034,12 @@ DSEL_API int dsel_index_score(const void* q, int dtype, int64_t tokens, int32_t 
   p.items = int32_t(groups * p.chunks);
   // A query an item, not too many of them to sum on the way in: every CTA takes the same number of tiles in one go,
   // however ragged the sequences.  (Ranges of 16 tiles dealt out: e4m3 decoding 167 us, an item's start costs four of
-  // its tiles; ranges of 32: the same, and bf16 262 us for 255, since some CTAs got one more than others.)
+  // its tiles; equal shares took 140; ranges of 32: the same, and bf16 262 us for 255, since some CTAs got one
+  // more than others.)
   // Where every tile has a CTA of its own, the sum would only come before it (1 x 8,192: 5.7 us for 4.8).
   const int64_t most_tiles = tokens * tiles;
   p.balanced = !wide && tokens <= 1024 && most_tiles > sms;
-  const int grid = p.balanced ? int(most_tiles < sms ? most_tiles : sms) : (p.items < sms ? p.items : sms);
+  const int grid = p.balanced ? sms : (p.items < sms ? p.items : sms);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return dtype == DSEL_E4M3 ? launch_type<true>(p, dtype, hp, wide, grid, smem, dev, cs)
                             : launch_type<false>(p, dtype, hp, wide, grid, smem, dev, cs);
