@@ -23,7 +23,7 @@
 //
 // Measured (one B200): 64 queries of 32 heads over 4, 32 blocks of 64 positions each 47 us
 // (269 MB, 0.88 of the copy rate); 1,024 queries of one sequence over 16 such blocks
-// 230 us (the 2.1 GB that they gather come out of L2 at 9.3 TB/s; 400 instructions a tile
+// 230 us (the 2.1 GB that they gather come out of L2 at 9.3 TB/s; 440 instructions a tile
 // of 16 bound it); 64 queries of 64 heads over one, 512 positions each 13.6 us (latency: the
 // index, the page, the row, then the join, each a round trip).
 #include <cstdint>
